@@ -482,6 +482,127 @@ MOE_API moe_status moe_ipc_close(void *base);
  * counterpart. */
 MOE_API moe_status moe_selftest_wait_timeout(void *ws, size_t ws_bytes, moe_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Microscaled (MX) experts: 4-bit weights, 8-bit (or 4-bit) activations.
+ * A row of values is cut into blocks of 32; each block has one scale, a
+ * power of two, and each value one code (OCP Microscaling Formats
+ * specification v1.0):
+ *   MOE_MX_E4M3  8-bit codes, one byte a value, largest value 448
+ *   MOE_MX_E2M1  4-bit codes (0 .5 1 1.5 2 3 4 6 and their negatives), two a
+ *                byte, the even column in the low half, largest value 6
+ *   scale byte c = 2^(c - 127); 255 is NaN
+ * Codes of a [rows, cols] matrix are rows of cols (or cols/2) bytes, scales
+ * rows of moe_mx_scale_pitch(cols) bytes, of which the first cols/32 count
+ * and the entry points below write the others as 0.
+ * Quantisation, wherever it is done below: the scale of a block is the
+ * smallest power of two, at least 2^-127, for which the block's largest
+ * magnitude is within the format's range (nothing saturates); a code is
+ * x / scale rounded to nearest, ties to even.  A block that holds a NaN or an
+ * infinity gets the scale byte 255 and codes 0, and so reads back as NaN.
+ * The pages' deployment section (jsqmd.com) asks for quantised experts with
+ * the router kept in higher precision; the router here stays bf16. */
+#define MOE_TYPE_BF16 0
+#define MOE_TYPE_FP16 1
+#define MOE_TYPE_FP32 2
+#define MOE_MX_E4M3 0
+#define MOE_MX_E2M1 1
+
+/* Bytes of a row of scales: cols/32 rounded up to a multiple of 16; 0 unless
+ * cols is a positive multiple of 32. */
+MOE_API int moe_mx_scale_pitch(int cols);
+
+/* Quantisation of rows.
+ *   x: rows of `type` (MOE_TYPE_*), x_stride elements apart (x_stride >= cols,
+ *     rows 16-byte aligned); cols a multiple of 32, rows * cols <= 2^34,
+ *     cols <= 2^20
+ *   fmt: MOE_MX_*; q out: codes; scales out: scale bytes
+ *   x_hat [rows, cols] of `type` out, or NULL: the values that codes and
+ *     scales stand for (exact, except where a scale reaches beyond the
+ *     range of `type`), to see what quantisation does to a matrix.
+ * Outputs must not overlap x or each other. */
+MOE_API moe_status moe_mx_quantize(long long rows, int cols, int type, const void *x,
+                                   long long x_stride, int fmt, uint8_t *q, uint8_t *scales,
+                                   void *x_hat, moe_stream_t stream);
+
+/* Residual addition and root-mean-square norm before the layer:
+ *   s = h + delta rounded to `type` (s = h without delta)
+ *   n_i = s_i / sqrt(mean_j s_j^2 + eps) * weight_i
+ * Sums and products are fp32 or wider; outputs are rounded once.
+ *   h: T rows of d values of `type`, h_stride elements apart; delta: T rows
+ *     of delta_type (`type` or MOE_TYPE_FP32, the type of moe_forward's out),
+ *     delta_stride elements apart, or NULL (delta_type and delta_stride are
+ *     then not looked at); weight [d] of `type`; eps > 0
+ *   h_out [T,d] out or NULL: s (may be h itself when h_stride == d)
+ *   y [T,d] of `type` out or NULL: n (the router's input)
+ *   q [T,d] and scales [T, pitch] out, or both NULL: n quantised to e4m3 (not
+ *     y: n is rounded once)
+ * At least one output.  d a multiple of 32, d <= 16384, 1 <= T <= 2^24; rows
+ * 16-byte aligned.  Apart from h_out == h, outputs must not overlap inputs
+ * or each other. */
+MOE_API moe_status moe_rmsnorm(int T, int d, int type, const void *h, long long h_stride,
+                               int delta_type, const void *delta, long long delta_stride,
+                               const void *weight, float eps, void *h_out, void *y, uint8_t *q,
+                               uint8_t *scales, moe_stream_t stream);
+
+/* Workspace bytes of moe_mx_product (N as there) and moe_mx_gated (N = d_ff);
+ * 0 if the sizes are unsupported.  At most 64 MiB. */
+MOE_API size_t moe_mx_workspace_size(int S, int E, int N);
+
+/* Product of microscaled rows with 4-bit expert weights: for every expert e
+ * and row r in [offsets[e], offsets[e+1])
+ *   y[r, n] = sum_k W_e[n, k] * x[r, k]
+ * with fp32 sums, rounded once to y_type (MOE_TYPE_BF16 or MOE_TYPE_FP32).
+ *   xq, xs: x [S,K] in x_fmt; Wq [E,N,K/2] e2m1 codes, Ws [E,N,pitch(K)] their
+ *   scales; offsets [E+1] int32 (device) as moe_permute returns them, or
+ *   NULL with E = 1: one segment of all S rows (a plain linear layer).
+ *   y [S,N] out; rows outside every segment are left as they were.
+ * K a multiple of 128, K <= 65536; N a multiple of 8, N <= 65536; 1 <= S <=
+ * 2^27, E <= 256, E * N < 2^31.  An inconsistent offsets array sets
+ * MOE_DEVERR_OFFSETS in the workspace's error word and no row is computed. */
+MOE_API moe_status moe_mx_product(int S, int K, int E, int N, int x_fmt, const uint8_t *xq,
+                                  const uint8_t *xs, const int32_t *offsets, const uint8_t *Wq,
+                                  const uint8_t *Ws, int y_type, void *y, void *ws,
+                                  size_t ws_bytes, moe_stream_t stream);
+
+/* The experts' up-projections with their activation, on microscaled rows:
+ *   h[r, f] = act(sum_i W1_e[f, i] x[r, i]) * (sum_i W3_e[f, i] x[r, i])
+ * with activation MOE_ACT_SILU (SwiGLU) or MOE_ACT_SIGMOID, sums and
+ * activation in fp32.  Either h [S,d_ff] bf16 out (hq and hs NULL), or hq
+ * [S,d_ff] and hs [S,pitch(d_ff)] out (h NULL): h quantised to e4m3, the
+ * input of the down projection with moe_mx_product.  W1q and W3q
+ * [E,d_ff,d/2], s1 and s3 [E,d_ff,pitch(d)]; the other arguments and the
+ * error word as in moe_mx_product.  d and d_ff multiples of 128, at most
+ * 65536. */
+MOE_API moe_status moe_mx_gated(int S, int d, int E, int d_ff, int x_fmt, const uint8_t *xq,
+                                const uint8_t *xs, const int32_t *offsets, const uint8_t *W1q,
+                                const uint8_t *s1, const uint8_t *W3q, const uint8_t *s3,
+                                int activation, moe_bf16 *h, uint8_t *hq, uint8_t *hs, void *ws,
+                                size_t ws_bytes, moe_stream_t stream);
+
+/* Workspace bytes of moe_forward_mx; 0 if the sizes are unsupported. */
+MOE_API size_t moe_forward_mx_workspace_size(int T, int d, int E, int d_ff, int k);
+
+/* A pre-norm MoE layer with microscaled experts in one call: moe_rmsnorm of
+ * h (+ delta) to bf16 rows for the router and e4m3 rows for the experts,
+ * moe_route, the dispatch of the 8-bit rows, moe_mx_gated (SwiGLU, e4m3 out),
+ * moe_mx_product (bf16 rows), and the gate-weighted combine:
+ *   x = norm(h + delta)
+ *   out[t] = sum_j w[t,j] * (W2_e (silu(W1_e x) * (W3_e x))), e = idx[t,j]
+ *   h [T,d] bf16; delta [T,d] fp32 or NULL (the previous layer's out);
+ *   norm_weight [d] bf16; eps > 0; h_out [T,d] bf16 out or NULL: h + delta
+ *   (may be h itself); Wg, router_bias as in moe_forward_ex; W1q, W3q
+ *   [E,d_ff,d/2], s1, s3 [E,d_ff,pitch(d)], W2q [E,d,d_ff/2], s2
+ *   [E,d,pitch(d_ff)]; out [T,d] fp32 out, not yet added to h_out: it is the
+ *   delta of what follows.
+ * Sizes as for moe_forward.  No shared expert.  The call can be captured in a
+ * CUDA graph. */
+MOE_API moe_status moe_forward_mx(int T, int d, int E, int d_ff, int k, const moe_bf16 *h,
+                                  const float *delta, const moe_bf16 *norm_weight, float eps,
+                                  moe_bf16 *h_out, const moe_bf16 *Wg, const float *router_bias,
+                                  const uint8_t *W1q, const uint8_t *s1, const uint8_t *W3q,
+                                  const uint8_t *s3, const uint8_t *W2q, const uint8_t *s2,
+                                  float *out, void *ws, size_t ws_bytes, moe_stream_t stream);
+
 /* Static description of a status code; never NULL. */
 MOE_API const char *moe_status_string(moe_status status);
 

@@ -35,7 +35,10 @@ ABI_FUNCTIONS = ("moe_workspace_size", "moe_workspace_size_ex", "moe_route", "mo
                  "moe_ep_workspace_size", "moe_ep_ffn_splits", "moe_ep_output_bf16",
                  "moe_ep_dispatch",
                  "moe_ep_expert_ffn", "moe_ep_combine", "moe_ipc_get_handle",
-                 "moe_ipc_open_handle", "moe_ipc_close", "moe_selftest_wait_timeout")
+                 "moe_ipc_open_handle", "moe_ipc_close", "moe_selftest_wait_timeout",
+                 "moe_mx_scale_pitch", "moe_mx_quantize", "moe_rmsnorm", "moe_mx_workspace_size",
+                 "moe_mx_product", "moe_mx_gated", "moe_forward_mx_workspace_size",
+                 "moe_forward_mx")
 TRACE_EVENTS = 6
 #: What each of moe_forward_traced's events marks (event i = start of stage i).
 TRACE_STAGES = ("route", "scatter", "expert_ffn", "shared_ffn", "combine")
@@ -44,6 +47,9 @@ TRACE_STAGES = ("route", "scatter", "expert_ffn", "shared_ffn", "combine")
 #: Gate-weight rules and expert activations of ``moe_variant`` (include/moe.h).
 WEIGHTS_SOFTMAX_TOPK, WEIGHTS_SOFTMAX_ALL, WEIGHTS_SIGMOID, WEIGHTS_ENTROPY = 0, 1, 2, 3
 ACT_SILU, ACT_SIGMOID = 0, 1
+#: Element types and microscaled formats (MOE_TYPE_*, MOE_MX_* of include/moe.h).
+TYPE_BF16, TYPE_FP16, TYPE_FP32 = 0, 1, 2
+MX_E4M3, MX_E2M1 = 0, 1
 
 
 class MoEVariant(ctypes.Structure):
@@ -62,6 +68,7 @@ _lib = None
 _lock = threading.Lock()
 
 _I, _P, _SZ = ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t
+_L, _F = ctypes.c_longlong, ctypes.c_float
 
 
 def load_library(path: str | None = None) -> ctypes.CDLL:
@@ -107,6 +114,14 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
             "moe_ipc_open_handle": (_I, [_P, _P]),
             "moe_ipc_close": (_I, [_P]),
             "moe_selftest_wait_timeout": (_I, [_P, _SZ, _P]),
+            "moe_mx_scale_pitch": (_I, [_I]),
+            "moe_mx_quantize": (_I, [_L, _I, _I, _P, _L, _I] + [_P] * 4),
+            "moe_rmsnorm": (_I, [_I] * 3 + [_P, _L, _I, _P, _L, _P, _F] + [_P] * 5),
+            "moe_mx_workspace_size": (_SZ, [_I] * 3),
+            "moe_mx_product": (_I, [_I] * 5 + [_P] * 5 + [_I, _P, _P, _SZ, _P]),
+            "moe_mx_gated": (_I, [_I] * 5 + [_P] * 7 + [_I] + [_P] * 4 + [_SZ, _P]),
+            "moe_forward_mx_workspace_size": (_SZ, [_I] * 5),
+            "moe_forward_mx": (_I, [_I] * 5 + [_P] * 3 + [_F] + [_P] * 11 + [_SZ, _P]),
         }
         for name, (res, args) in sig.items():
             f = getattr(lib, name)
@@ -370,3 +385,60 @@ def moe_selftest_wait_timeout(ws, stream=None):
     result with moe_get_device_error(ws)."""
     _check(load_library().moe_selftest_wait_timeout(_ptr(ws), _ws_bytes(ws), _stream(stream)),
            "moe_selftest_wait_timeout")
+
+
+# --------------------------------------------------- microscaled (MX) experts
+
+def moe_mx_scale_pitch(cols) -> int:
+    """Bytes of a row of scales of ``cols`` values (0 unless a multiple of 32)."""
+    return int(load_library().moe_mx_scale_pitch(cols))
+
+
+def moe_mx_quantize(rows, cols, type, x, x_stride, fmt, q, scales, x_hat=None, stream=None):
+    """``type``: TYPE_*, ``fmt``: MX_*; ``q`` and ``scales`` uint8 out,
+    ``x_hat`` the values they stand for (include/moe.h)."""
+    _check(load_library().moe_mx_quantize(rows, cols, type, _ptr(x), x_stride, fmt, _ptr(q),
+                                          _ptr(scales), _ptr(x_hat), _stream(stream)),
+           "moe_mx_quantize")
+
+
+def moe_rmsnorm(T, d, type, h, h_stride, delta_type, delta, delta_stride, weight, eps, h_out, y, q,
+                scales, stream=None):
+    """``h_out``, ``y`` and the pair ``q``, ``scales`` may each be None."""
+    _check(load_library().moe_rmsnorm(T, d, type, _ptr(h), h_stride, delta_type, _ptr(delta),
+                                      delta_stride, _ptr(weight), eps, _ptr(h_out), _ptr(y),
+                                      _ptr(q), _ptr(scales), _stream(stream)), "moe_rmsnorm")
+
+
+def moe_mx_workspace_size(S, E, N) -> int:
+    return int(load_library().moe_mx_workspace_size(S, E, N))
+
+
+def moe_mx_product(S, K, E, N, x_fmt, xq, xs, offsets, Wq, Ws, y_type, y, ws, stream=None):
+    _check(load_library().moe_mx_product(S, K, E, N, x_fmt, _ptr(xq), _ptr(xs), _ptr(offsets),
+                                         _ptr(Wq), _ptr(Ws), y_type, _ptr(y), _ptr(ws),
+                                         _ws_bytes(ws), _stream(stream)), "moe_mx_product")
+
+
+def moe_mx_gated(S, d, E, d_ff, x_fmt, xq, xs, offsets, W1q, s1, W3q, s3, activation, h, hq, hs, ws,
+                 stream=None):
+    """Either ``h`` (bf16) or the pair ``hq``, ``hs`` (e4m3) is given."""
+    _check(load_library().moe_mx_gated(S, d, E, d_ff, x_fmt, _ptr(xq), _ptr(xs), _ptr(offsets),
+                                       _ptr(W1q), _ptr(s1), _ptr(W3q), _ptr(s3), activation,
+                                       _ptr(h), _ptr(hq), _ptr(hs), _ptr(ws), _ws_bytes(ws),
+                                       _stream(stream)), "moe_mx_gated")
+
+
+def moe_forward_mx_workspace_size(T, d, E, d_ff, k) -> int:
+    return int(load_library().moe_forward_mx_workspace_size(T, d, E, d_ff, k))
+
+
+def moe_forward_mx(T, d, E, d_ff, k, h, delta, norm_weight, eps, h_out, Wg, router_bias, W1q, s1,
+                   W3q, s3, W2q, s2, out, ws, stream=None):
+    """Norm, router, MX experts and combine; ``delta``, ``h_out`` and
+    ``router_bias`` may be None (include/moe.h)."""
+    _check(load_library().moe_forward_mx(T, d, E, d_ff, k, _ptr(h), _ptr(delta),
+                                         _ptr(norm_weight), eps, _ptr(h_out), _ptr(Wg),
+                                         _ptr(router_bias), _ptr(W1q), _ptr(s1), _ptr(W3q),
+                                         _ptr(s3), _ptr(W2q), _ptr(s2), _ptr(out), _ptr(ws),
+                                         _ws_bytes(ws), _stream(stream)), "moe_forward_mx")

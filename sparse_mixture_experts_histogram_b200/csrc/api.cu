@@ -13,6 +13,7 @@
 
 #include "internal.h"
 #include "moe.h"
+#include "mx.cuh"
 
 namespace moe {
 
@@ -967,6 +968,351 @@ moe_status moe_get_device_error(const void *ws, uint32_t *code, moe_stream_t str
     return MOE_ERR_DEVICE;
 }
 
+
+// --------------------------------------------------- microscaled (MX) experts
+
+int moe_mx_scale_pitch(int cols) { return cols > 0 && cols % kMxBlock == 0 ? mx_scale_pitch(cols) : 0; }
+
+static bool mx_type(int t) { return t == MOE_TYPE_BF16 || t == MOE_TYPE_FP16 || t == MOE_TYPE_FP32; }
+static bool mx_fmt(int f) { return f == MOE_MX_E4M3 || f == MOE_MX_E2M1; }
+
+// Rows `stride` elements of `type` apart that start on 16-byte boundaries.
+static bool mx_rows(const void *p, int type, int cols, long long stride)
+{
+    const long long size = type == MOE_TYPE_FP32 ? 4 : 2;
+    return ok_ptr(p) && stride >= cols && stride <= (1LL << 40) && stride * size % 16 == 0;
+}
+
+moe_status moe_mx_quantize(long long rows, int cols, int type, const void *x, long long x_stride,
+                           int fmt, uint8_t *q, uint8_t *scales, void *x_hat, moe_stream_t stream)
+{
+    if (rows < 1 || cols < 1 || !mx_type(type) || !mx_fmt(fmt)) return MOE_ERR_INVALID_ARG;
+    if (cols % kMxBlock || cols > (1 << 20) || rows > (1LL << 34) / cols) return MOE_ERR_UNSUPPORTED;
+    if (!mx_rows(x, type, cols, x_stride) || !ok_ptr(q) || !ok_ptr(scales)) return MOE_ERR_INVALID_ARG;
+    if (x_hat != nullptr && !aligned16(x_hat)) return MOE_ERR_INVALID_ARG;
+    MxQuantLaunch a{};
+    a.rows = rows;
+    a.cols = cols;
+    a.type = type;
+    a.fmt = fmt;
+    a.x = x;
+    a.x_stride = x_stride;
+    a.q = q;
+    a.scales = scales;
+    a.hat = x_hat;
+    a.pdl = true;
+    return from_cuda(launch_mx_quantize(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+moe_status moe_rmsnorm(int T, int d, int type, const void *h, long long h_stride, int delta_type,
+                       const void *delta, long long delta_stride, const void *weight, float eps,
+                       void *h_out, void *y, uint8_t *q, uint8_t *scales, moe_stream_t stream)
+{
+    if (T < 1 || d < 1 || !mx_type(type)) return MOE_ERR_INVALID_ARG;
+    if (!(eps > 0.0f) || !std::isfinite(eps)) return MOE_ERR_INVALID_ARG;
+    if (T > (1 << 24) || d % kMxBlock || d > 16384) return MOE_ERR_UNSUPPORTED;
+    if (!mx_rows(h, type, d, h_stride) || !ok_ptr(weight)) return MOE_ERR_INVALID_ARG;
+    if (delta != nullptr) {
+        if (delta_type != type && delta_type != MOE_TYPE_FP32) return MOE_ERR_INVALID_ARG;
+        if (!mx_rows(delta, delta_type, d, delta_stride)) return MOE_ERR_INVALID_ARG;
+    }
+    if ((q == nullptr) != (scales == nullptr)) return MOE_ERR_INVALID_ARG;
+    if (h_out == nullptr && y == nullptr && q == nullptr) return MOE_ERR_INVALID_ARG;
+    if (!aligned16(h_out) || !aligned16(y) || !aligned16(q) || !aligned16(scales))
+        return MOE_ERR_INVALID_ARG;
+    if (h_out == h && h_stride != d) return MOE_ERR_INVALID_ARG;
+    NormLaunch a{};
+    a.T = T;
+    a.d = d;
+    a.type = type;
+    a.h = h;
+    a.h_stride = h_stride;
+    a.delta_type = delta_type;
+    a.delta = delta;
+    a.delta_stride = delta == nullptr ? 0 : delta_stride;
+    a.w = weight;
+    a.eps = eps;
+    a.h_out = h_out;
+    a.y = y;
+    a.q = q;
+    a.scales = scales;
+    a.q_stride = d;
+    a.s_stride = mx_scale_pitch(d);
+    a.pdl = true;
+    return from_cuda(launch_rmsnorm(a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+// Sizes of a product: S rows, K the summed width, E * N weight rows.
+static moe_status mx_check(int S, int K, int E, int N, int n_step)
+{
+    if (S < 1 || K < 1 || E < 1 || N < 1) return MOE_ERR_INVALID_ARG;
+    if (S > (1 << 27) || E > 256 || K % 128 || K > 65536 || N % n_step || N > 65536)
+        return MOE_ERR_UNSUPPORTED;
+    return MOE_OK;
+}
+
+size_t moe_mx_workspace_size(int S, int E, int N)
+{
+    if (mx_check(S, 128, E, N, 8) != MOE_OK) return 0;
+    return kHeaderBytes + mx_gemm_scratch_bytes(S, E, N);
+}
+
+static moe_status mx_gemm(MxGemmLaunch &a, void *ws, size_t ws_bytes, moe_stream_t stream)
+{
+    if (a.offsets == nullptr ? a.E != 1 : !aligned16(a.offsets)) return MOE_ERR_INVALID_ARG;
+    if (!ok_ptr(ws) || reinterpret_cast<uintptr_t>(ws) % kAlign) return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < moe_mx_workspace_size(a.S, a.E, a.N)) return MOE_ERR_WORKSPACE;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    uint8_t *wsb = static_cast<uint8_t *>(ws);
+    a.x_stride = a.fmt == MOE_MX_E4M3 ? a.K : a.K / 2;
+    a.xs_stride = mx_scale_pitch(a.K);
+    a.err = reinterpret_cast<uint32_t *>(wsb);
+    a.scratch = wsb + kHeaderBytes;
+    const moe_status st = from_cuda(
+        cudaMemsetAsync(wsb, 0, kHeaderBytes + mx_gemm_zero_bytes(a.S, a.E, a.N), s));
+    if (st != MOE_OK) return st;
+    return from_cuda(launch_mx_gemm(a, s));
+}
+
+moe_status moe_mx_product(int S, int K, int E, int N, int x_fmt, const uint8_t *xq,
+                          const uint8_t *xs, const int32_t *offsets, const uint8_t *Wq,
+                          const uint8_t *Ws, int y_type, void *y, void *ws, size_t ws_bytes,
+                          moe_stream_t stream)
+{
+    const moe_status st = mx_check(S, K, E, N, 8);
+    if (st != MOE_OK) return st;
+    if (!mx_fmt(x_fmt) || (y_type != MOE_TYPE_BF16 && y_type != MOE_TYPE_FP32))
+        return MOE_ERR_INVALID_ARG;
+    if (!ok_ptr(xq) || !ok_ptr(xs) || !ok_ptr(Wq) || !ok_ptr(Ws) || !ok_ptr(y))
+        return MOE_ERR_INVALID_ARG;
+    MxGemmLaunch a{};
+    a.S = S;
+    a.K = K;
+    a.E = E;
+    a.N = N;
+    a.fmt = x_fmt;
+    a.x = xq;
+    a.xs = xs;
+    a.offsets = offsets;
+    a.W1 = Wq;
+    a.s1 = Ws;
+    a.y_type = y_type;
+    a.y = y;
+    return mx_gemm(a, ws, ws_bytes, stream);
+}
+
+moe_status moe_mx_gated(int S, int d, int E, int d_ff, int x_fmt, const uint8_t *xq,
+                        const uint8_t *xs, const int32_t *offsets, const uint8_t *W1q,
+                        const uint8_t *s1, const uint8_t *W3q, const uint8_t *s3, int activation,
+                        moe_bf16 *h, uint8_t *hq, uint8_t *hs, void *ws, size_t ws_bytes,
+                        moe_stream_t stream)
+{
+    const moe_status st = mx_check(S, d, E, d_ff, 128);
+    if (st != MOE_OK) return st;
+    if (!mx_fmt(x_fmt) || (activation != MOE_ACT_SILU && activation != MOE_ACT_SIGMOID))
+        return MOE_ERR_INVALID_ARG;
+    if (!ok_ptr(xq) || !ok_ptr(xs) || !ok_ptr(W1q) || !ok_ptr(s1) || !ok_ptr(W3q) || !ok_ptr(s3))
+        return MOE_ERR_INVALID_ARG;
+    if (h != nullptr ? !aligned16(h) || hq != nullptr || hs != nullptr : !ok_ptr(hq) || !ok_ptr(hs))
+        return MOE_ERR_INVALID_ARG;
+    MxGemmLaunch a{};
+    a.S = S;
+    a.K = d;
+    a.E = E;
+    a.N = d_ff;
+    a.fmt = x_fmt;
+    a.x = xq;
+    a.xs = xs;
+    a.offsets = offsets;
+    a.W1 = W1q;
+    a.s1 = s1;
+    a.W3 = W3q;
+    a.s3 = s3;
+    a.act = activation == MOE_ACT_SIGMOID ? 1 : 0;
+    a.y_type = MOE_TYPE_BF16;
+    a.y = h;
+    a.q = hq;
+    a.qs = hs;
+    return mx_gemm(a, ws, ws_bytes, stream);
+}
+
+// Workspace of moe_forward_mx: the header and counters (cleared at the start
+// of every call), the router's arrays, and the layer's intermediates.  A
+// token's 8-bit row and its scales lie side by side (xrow bytes), so that one
+// copy moves both to the expert's segment.
+struct MxForwardLayout {
+    Layout r;
+    size_t up, down;                 // scratch of the two products
+    size_t x, x8, x8p, hq, hs, y, total;
+    int xrow;
+};
+
+static MxForwardLayout mx_forward_layout(int T, int d, int E, int d_ff, int k)
+{
+    MxForwardLayout L{};
+    size_t o = kHeaderBytes;
+    auto take = [&](size_t bytes) {
+        const size_t r = o;
+        o += align_up(bytes);
+        return r;
+    };
+    const int Sn = T * k;
+    const size_t S = static_cast<size_t>(Sn);
+    const size_t ntiles = (static_cast<size_t>(T) + 127) / 128;
+    L.xrow = d + mx_scale_pitch(d);
+    L.r.tilectr = take(ntiles * 4);
+    const size_t zu = mx_gemm_zero_bytes(Sn, E, d_ff), zd = mx_gemm_zero_bytes(Sn, E, d);
+    // The counters of both products are cleared with the header; the rest of
+    // their scratch follows them.
+    L.up = take(zu);
+    L.down = take(zd);
+    L.r.zero_bytes = o;
+    L.r.tilecnt = take(ntiles * E * 4);
+    L.r.tilebase = take(ntiles * E * 4);
+    L.r.rank = take(S * 4);
+    L.r.offsets = take((static_cast<size_t>(E) + 1) * 4);
+    L.r.counts = take(static_cast<size_t>(E) * 4);
+    L.r.idx = take(S * 4);
+    L.r.w = take(S * 4);
+    L.r.row = take(S * 4);
+    L.x = take(static_cast<size_t>(T) * d * 2);
+    L.x8 = take(static_cast<size_t>(T) * L.xrow);
+    L.x8p = take(S * L.xrow);
+    L.hq = take(S * d_ff);
+    L.hs = take(S * mx_scale_pitch(d_ff));
+    L.y = take(S * d * 2);
+    L.total = o;
+    return L;
+}
+
+size_t moe_forward_mx_workspace_size(int T, int d, int E, int d_ff, int k)
+{
+    if (check_shapes(T, d, E, d_ff, k, 0) != MOE_OK) return 0;
+    return mx_forward_layout(T, d, E, d_ff, k).total;
+}
+
+moe_status moe_forward_mx(int T, int d, int E, int d_ff, int k, const moe_bf16 *h,
+                          const float *delta, const moe_bf16 *norm_weight, float eps,
+                          moe_bf16 *h_out, const moe_bf16 *Wg, const float *router_bias,
+                          const uint8_t *W1q, const uint8_t *s1, const uint8_t *W3q,
+                          const uint8_t *s3, const uint8_t *W2q, const uint8_t *s2, float *out,
+                          void *ws, size_t ws_bytes, moe_stream_t stream)
+{
+    moe_status st = check_shapes(T, d, E, d_ff, k, 0);
+    if (st != MOE_OK) return st;
+    if (!(eps > 0.0f) || !std::isfinite(eps)) return MOE_ERR_INVALID_ARG;
+    if (!ok_ptr(h) || !ok_ptr(norm_weight) || !ok_ptr(Wg) || !ok_ptr(W1q) || !ok_ptr(s1) ||
+        !ok_ptr(W3q) || !ok_ptr(s3) || !ok_ptr(W2q) || !ok_ptr(s2) || !ok_ptr(out) || !ok_ptr(ws))
+        return MOE_ERR_INVALID_ARG;
+    if (!aligned16(delta) || !aligned16(h_out) || !aligned16(router_bias))
+        return MOE_ERR_INVALID_ARG;
+    if (reinterpret_cast<uintptr_t>(ws) % kAlign) return MOE_ERR_INVALID_ARG;
+    const MxForwardLayout L = mx_forward_layout(T, d, E, d_ff, k);
+    if (ws_bytes < L.total) return MOE_ERR_WORKSPACE;
+
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    uint8_t *wsb = static_cast<uint8_t *>(ws);
+    uint32_t *err = reinterpret_cast<uint32_t *>(wsb);
+    int32_t *idx = reinterpret_cast<int32_t *>(wsb + L.r.idx);
+    float *w = reinterpret_cast<float *>(wsb + L.r.w);
+    int32_t *offsets = reinterpret_cast<int32_t *>(wsb + L.r.offsets);
+    int32_t *row = reinterpret_cast<int32_t *>(wsb + L.r.row);
+    uint16_t *x = reinterpret_cast<uint16_t *>(wsb + L.x);
+    st = from_cuda(cudaMemsetAsync(wsb, 0, L.r.zero_bytes, s));
+    if (st != MOE_OK) return st;
+
+    NormLaunch n{};
+    n.T = T;
+    n.d = d;
+    n.type = MOE_TYPE_BF16;
+    n.h = h;
+    n.h_stride = d;
+    n.delta_type = MOE_TYPE_FP32;
+    n.delta = delta;
+    n.delta_stride = d;
+    n.w = norm_weight;
+    n.eps = eps;
+    n.h_out = h_out;
+    n.y = x;
+    n.q = wsb + L.x8;
+    n.scales = wsb + L.x8 + d;
+    n.q_stride = n.s_stride = L.xrow;
+    st = from_cuda(launch_rmsnorm(n, s));
+    if (st != MOE_OK) return st;
+    st = route_impl(T, d, E, k, x, Wg, router_bias, idx, w,
+                    reinterpret_cast<int32_t *>(wsb + L.r.counts), offsets, wsb, L.r, s);
+    if (st != MOE_OK) return st;
+    ScatterLaunch c{};
+    c.cap = -1;
+    c.T = T;
+    c.d = L.xrow / 2;  // rows of xrow bytes, copied as 16-bit elements
+    c.E = E;
+    c.k = k;
+    c.x = reinterpret_cast<const uint16_t *>(wsb + L.x8);
+    c.idx = idx;
+    c.rank = reinterpret_cast<int32_t *>(wsb + L.r.rank);
+    c.tilebase = reinterpret_cast<int32_t *>(wsb + L.r.tilebase);
+    c.x_perm = reinterpret_cast<uint16_t *>(wsb + L.x8p);
+    c.row_of_slot = row;
+    c.err = err;
+    c.pdl = true;
+    st = from_cuda(launch_scatter(c, s));
+    if (st != MOE_OK) return st;
+    MxGemmLaunch a{};
+    a.S = T * k;
+    a.K = d;
+    a.E = E;
+    a.N = d_ff;
+    a.fmt = MOE_MX_E4M3;
+    a.x = wsb + L.x8p;
+    a.xs = wsb + L.x8p + d;
+    a.x_stride = a.xs_stride = L.xrow;
+    a.offsets = offsets;
+    a.W1 = W1q;
+    a.s1 = s1;
+    a.W3 = W3q;
+    a.s3 = s3;
+    a.y_type = MOE_TYPE_BF16;
+    a.q = wsb + L.hq;
+    a.qs = wsb + L.hs;
+    a.scratch = wsb + L.up;
+    a.err = err;
+    a.pdl = true;
+    st = from_cuda(launch_mx_gemm(a, s));
+    if (st != MOE_OK) return st;
+    MxGemmLaunch b{};
+    b.S = T * k;
+    b.K = d_ff;
+    b.E = E;
+    b.N = d;
+    b.fmt = MOE_MX_E4M3;
+    b.x = wsb + L.hq;
+    b.xs = wsb + L.hs;
+    b.x_stride = d_ff;
+    b.xs_stride = mx_scale_pitch(d_ff);
+    b.offsets = offsets;
+    b.W1 = W2q;
+    b.s1 = s2;
+    b.y_type = MOE_TYPE_BF16;
+    b.y = wsb + L.y;
+    b.scratch = wsb + L.down;
+    b.err = err;
+    b.pdl = true;
+    st = from_cuda(launch_mx_gemm(b, s));
+    if (st != MOE_OK) return st;
+    CombineLaunch cb{};
+    cb.T = T;
+    cb.d = d;
+    cb.k = k;
+    cb.ksplit = 1;
+    cb.y = reinterpret_cast<const float *>(wsb + L.y);
+    cb.y_bf16 = true;
+    cb.row_of_slot = row;
+    cb.w = w;
+    cb.out = out;
+    cb.pdl = true;
+    return from_cuda(launch_combine(cb, s));
+}
 
 // ------------------------------------------------------- expert parallelism
 

@@ -158,6 +158,58 @@ struct EpCombineLaunch {
 cudaError_t launch_ep_dispatch(const EpDispatchLaunch &a, cudaStream_t s);
 cudaError_t launch_ep_combine(const EpCombineLaunch &a, cudaStream_t s);
 
+// Microscaled (MX) operators (mx_rows.cu, mx_gemm.cu).  Types and formats are
+// the C ABI's MOE_TYPE_* and MOE_MX_* values; strides of h, delta and x are
+// in elements, of q and scales in bytes.
+struct NormLaunch {
+    int T, d, type;
+    const void *h;            // [T, d]
+    long long h_stride;
+    int delta_type;           // type, or fp32
+    const void *delta;        // [T, d] or nullptr
+    long long delta_stride;
+    const void *w;            // [d]
+    float eps;
+    void *h_out, *y;          // [T, d] or nullptr
+    uint8_t *q, *scales;      // e4m3 codes and scale bytes, or both nullptr
+    long long q_stride, s_stride;
+    bool pdl;
+};
+
+struct MxQuantLaunch {
+    long long rows;
+    int cols, type, fmt;
+    const void *x;
+    long long x_stride;
+    uint8_t *q, *scales;
+    void *hat;                // [rows, cols] or nullptr
+    bool pdl;
+};
+
+struct MxGemmLaunch {
+    int S, K, E, N;           // N rows of W1 (and of W3) per expert
+    int fmt;                  // format of x
+    const uint8_t *x, *xs;    // row strides in bytes below
+    long long x_stride, xs_stride;
+    const int32_t *offsets;   // [E+1] or nullptr (one segment [0, S), E = 1)
+    const uint8_t *W1, *s1;   // e2m1 [E, N, K/2], scales [E, N, pitch(K)]
+    const uint8_t *W3, *s3;   // or nullptr: the plain product
+    int act;                  // gated: 0 silu(W1 x) * W3 x, 1 sigmoid(W1 x) * W3 x
+    int y_type;
+    void *y;                  // [S, N] bf16 or fp32, or nullptr (gated, e4m3 out)
+    uint8_t *q, *qs;          // [S, N] e4m3 and scale bytes [S, pitch(N)]
+    uint8_t *scratch;         // mx_gemm_scratch_bytes(), counters zero before the launch
+    uint32_t *err;
+    bool pdl;
+};
+
+// Scratch of one product: its first mx_gemm_zero_bytes() are counters.
+size_t mx_gemm_scratch_bytes(int S, int E, int N);
+size_t mx_gemm_zero_bytes(int S, int E, int N);
+cudaError_t launch_rmsnorm(const NormLaunch &a, cudaStream_t s);
+cudaError_t launch_mx_quantize(const MxQuantLaunch &a, cudaStream_t s);
+cudaError_t launch_mx_gemm(const MxGemmLaunch &a, cudaStream_t s);
+
 // Failure-detection self-test (selftest.cu): a bounded wait that runs out.
 cudaError_t launch_wait_timeout(uint32_t *err, cudaStream_t s);
 
