@@ -552,8 +552,8 @@ MOE_API size_t moe_mx_workspace_size(int S, int E, int N);
  * and row r in [offsets[e], offsets[e+1])
  *   y[r, n] = sum_k W_e[n, k] * x[r, k]
  * with fp32 sums, rounded once to y_type (MOE_TYPE_BF16 or MOE_TYPE_FP32).
- *   xq, xs: x [S,K] in x_fmt; Wq [E,N,K/2] e2m1 codes, Ws [E,N,pitch(K)] their
- *   scales; offsets [E+1] int32 (device) as moe_permute returns them, or
+ *   xq, xs: x [S,K] in x_fmt; Wq [E,N,K/2] e2m1 codes (32-byte aligned, as
+ *   all 4-bit weights), Ws [E,N,pitch(K)] their scales; offsets [E+1] int32 (device) as moe_permute returns them, or
  *   NULL with E = 1: one segment of all S rows (a plain linear layer).
  *   y [S,N] out; rows outside every segment are left as they were.
  * K a multiple of 128, K <= 65536; N a multiple of 8, N <= 65536; 1 <= S <=

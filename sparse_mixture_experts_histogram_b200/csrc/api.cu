@@ -103,6 +103,7 @@ moe_status check_shapes(int T, int d, int E, int d_ff, int k, int d_ffs)
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool ok_ptr(const void *p) { return p != nullptr && aligned16(p); }
+bool ok_ptr32(const void *p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 31u) == 0; }
 
 moe_status from_cuda(cudaError_t e) { return e == cudaSuccess ? MOE_OK : MOE_ERR_CUDA; }
 
@@ -217,6 +218,40 @@ cudaError_t make_tmap_f16_atoms(CUtensorMap *map, const void *base, uint64_t row
                                 dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t make_tmap_rows(CUtensorMap *map, const void *base, uint64_t rows, uint64_t bytes,
+                           uint64_t stride, uint32_t box_bytes, uint32_t box_rows)
+{
+    std::call_once(g_encode_once, load_encode);
+    if (g_encode == nullptr) return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {bytes, rows};
+    const cuuint64_t strides[1] = {stride};
+    const cuuint32_t box[2] = {box_bytes, box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base),
+                                dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+                                box_bytes == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_256B
+                                                 : CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t make_tmap_e2m1_wide(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols,
+                                uint32_t box_rows)
+{
+    std::call_once(g_encode_once, load_encode);
+    if (g_encode == nullptr) return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {cols, rows};
+    const cuuint64_t strides[1] = {cols / 2};
+    const cuuint32_t box[2] = {128, box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r =
+        g_encode(map, CU_TENSOR_MAP_DATA_TYPE_16U4_ALIGN16B, 2, const_cast<void *>(base), dims,
+                 strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
@@ -1054,7 +1089,7 @@ static moe_status mx_check(int S, int K, int E, int N, int n_step)
 size_t moe_mx_workspace_size(int S, int E, int N)
 {
     if (mx_check(S, 128, E, N, 8) != MOE_OK) return 0;
-    return kHeaderBytes + mx_gemm_scratch_bytes(S, E, N);
+    return kHeaderBytes + align_up(mx_gemm_zero_bytes()) + mx_gemm_scratch_bytes(S);
 }
 
 static moe_status mx_gemm(MxGemmLaunch &a, void *ws, size_t ws_bytes, moe_stream_t stream)
@@ -1067,9 +1102,10 @@ static moe_status mx_gemm(MxGemmLaunch &a, void *ws, size_t ws_bytes, moe_stream
     a.x_stride = a.fmt == MOE_MX_E4M3 ? a.K : a.K / 2;
     a.xs_stride = mx_scale_pitch(a.K);
     a.err = reinterpret_cast<uint32_t *>(wsb);
-    a.scratch = wsb + kHeaderBytes;
-    const moe_status st = from_cuda(
-        cudaMemsetAsync(wsb, 0, kHeaderBytes + mx_gemm_zero_bytes(a.S, a.E, a.N), s));
+    a.counters = wsb + kHeaderBytes;
+    a.scratch = a.counters + align_up(mx_gemm_zero_bytes());
+    const moe_status st =
+        from_cuda(cudaMemsetAsync(wsb, 0, kHeaderBytes + mx_gemm_zero_bytes(), s));
     if (st != MOE_OK) return st;
     return from_cuda(launch_mx_gemm(a, s));
 }
@@ -1083,7 +1119,7 @@ moe_status moe_mx_product(int S, int K, int E, int N, int x_fmt, const uint8_t *
     if (st != MOE_OK) return st;
     if (!mx_fmt(x_fmt) || (y_type != MOE_TYPE_BF16 && y_type != MOE_TYPE_FP32))
         return MOE_ERR_INVALID_ARG;
-    if (!ok_ptr(xq) || !ok_ptr(xs) || !ok_ptr(Wq) || !ok_ptr(Ws) || !ok_ptr(y))
+    if (!ok_ptr(xq) || !ok_ptr(xs) || !ok_ptr32(Wq) || !ok_ptr(Ws) || !ok_ptr(y))
         return MOE_ERR_INVALID_ARG;
     MxGemmLaunch a{};
     a.S = S;
@@ -1111,7 +1147,7 @@ moe_status moe_mx_gated(int S, int d, int E, int d_ff, int x_fmt, const uint8_t 
     if (st != MOE_OK) return st;
     if (!mx_fmt(x_fmt) || (activation != MOE_ACT_SILU && activation != MOE_ACT_SIGMOID))
         return MOE_ERR_INVALID_ARG;
-    if (!ok_ptr(xq) || !ok_ptr(xs) || !ok_ptr(W1q) || !ok_ptr(s1) || !ok_ptr(W3q) || !ok_ptr(s3))
+    if (!ok_ptr(xq) || !ok_ptr(xs) || !ok_ptr32(W1q) || !ok_ptr(s1) || !ok_ptr32(W3q) || !ok_ptr(s3))
         return MOE_ERR_INVALID_ARG;
     if (h != nullptr ? !aligned16(h) || hq != nullptr || hs != nullptr : !ok_ptr(hq) || !ok_ptr(hs))
         return MOE_ERR_INVALID_ARG;
@@ -1142,8 +1178,8 @@ moe_status moe_mx_gated(int S, int d, int E, int d_ff, int x_fmt, const uint8_t 
 // copy moves both to the expert's segment.
 struct MxForwardLayout {
     Layout r;
-    size_t up, down;                 // scratch of the two products
-    size_t x, x8, x8p, hq, hs, y, total;
+    size_t up, down;                 // counters of the two products
+    size_t x, x8, x8p, hq, hs, y, parts, total;
     int xrow;
 };
 
@@ -1156,16 +1192,12 @@ static MxForwardLayout mx_forward_layout(int T, int d, int E, int d_ff, int k)
         o += align_up(bytes);
         return r;
     };
-    const int Sn = T * k;
-    const size_t S = static_cast<size_t>(Sn);
+    const size_t S = static_cast<size_t>(T) * k;
     const size_t ntiles = (static_cast<size_t>(T) + 127) / 128;
     L.xrow = d + mx_scale_pitch(d);
     L.r.tilectr = take(ntiles * 4);
-    const size_t zu = mx_gemm_zero_bytes(Sn, E, d_ff), zd = mx_gemm_zero_bytes(Sn, E, d);
-    // The counters of both products are cleared with the header; the rest of
-    // their scratch follows them.
-    L.up = take(zu);
-    L.down = take(zd);
+    L.up = take(mx_gemm_zero_bytes());
+    L.down = take(mx_gemm_zero_bytes());
     L.r.zero_bytes = o;
     L.r.tilecnt = take(ntiles * E * 4);
     L.r.tilebase = take(ntiles * E * 4);
@@ -1181,6 +1213,7 @@ static MxForwardLayout mx_forward_layout(int T, int d, int E, int d_ff, int k)
     L.hq = take(S * d_ff);
     L.hs = take(S * mx_scale_pitch(d_ff));
     L.y = take(S * d * 2);
+    L.parts = take(mx_gemm_scratch_bytes(T * k));  // of one product after the other
     L.total = o;
     return L;
 }
@@ -1201,8 +1234,8 @@ moe_status moe_forward_mx(int T, int d, int E, int d_ff, int k, const moe_bf16 *
     moe_status st = check_shapes(T, d, E, d_ff, k, 0);
     if (st != MOE_OK) return st;
     if (!(eps > 0.0f) || !std::isfinite(eps)) return MOE_ERR_INVALID_ARG;
-    if (!ok_ptr(h) || !ok_ptr(norm_weight) || !ok_ptr(Wg) || !ok_ptr(W1q) || !ok_ptr(s1) ||
-        !ok_ptr(W3q) || !ok_ptr(s3) || !ok_ptr(W2q) || !ok_ptr(s2) || !ok_ptr(out) || !ok_ptr(ws))
+    if (!ok_ptr(h) || !ok_ptr(norm_weight) || !ok_ptr(Wg) || !ok_ptr32(W1q) || !ok_ptr(s1) ||
+        !ok_ptr32(W3q) || !ok_ptr(s3) || !ok_ptr32(W2q) || !ok_ptr(s2) || !ok_ptr(out) || !ok_ptr(ws))
         return MOE_ERR_INVALID_ARG;
     if (!aligned16(delta) || !aligned16(h_out) || !aligned16(router_bias))
         return MOE_ERR_INVALID_ARG;
@@ -1275,7 +1308,8 @@ moe_status moe_forward_mx(int T, int d, int E, int d_ff, int k, const moe_bf16 *
     a.y_type = MOE_TYPE_BF16;
     a.q = wsb + L.hq;
     a.qs = wsb + L.hs;
-    a.scratch = wsb + L.up;
+    a.counters = wsb + L.up;
+    a.scratch = wsb + L.parts;
     a.err = err;
     a.pdl = true;
     st = from_cuda(launch_mx_gemm(a, s));
@@ -1295,7 +1329,8 @@ moe_status moe_forward_mx(int T, int d, int E, int d_ff, int k, const moe_bf16 *
     b.s1 = s2;
     b.y_type = MOE_TYPE_BF16;
     b.y = wsb + L.y;
-    b.scratch = wsb + L.down;
+    b.counters = wsb + L.down;
+    b.scratch = wsb + L.parts;
     b.err = err;
     b.pdl = true;
     st = from_cuda(launch_mx_gemm(b, s));

@@ -198,14 +198,25 @@ struct MxGemmLaunch {
     int y_type;
     void *y;                  // [S, N] bf16 or fp32, or nullptr (gated, e4m3 out)
     uint8_t *q, *qs;          // [S, N] e4m3 and scale bytes [S, pitch(N)]
-    uint8_t *scratch;         // mx_gemm_scratch_bytes(), counters zero before the launch
+    uint8_t *counters;        // mx_gemm_zero_bytes(), zero before the launch
+    uint8_t *scratch;         // mx_gemm_scratch_bytes()
     uint32_t *err;
     bool pdl;
 };
 
-// Scratch of one product: its first mx_gemm_zero_bytes() are counters.
-size_t mx_gemm_scratch_bytes(int S, int E, int N);
-size_t mx_gemm_zero_bytes(int S, int E, int N);
+// Tensor map of `rows` rows of `bytes` bytes, `stride` bytes apart: boxes of
+// box_bytes x box_rows, 128-byte swizzled when box_bytes is 128.
+cudaError_t make_tmap_rows(CUtensorMap *map, const void *base, uint64_t rows, uint64_t bytes,
+                           uint64_t stride, uint32_t box_bytes, uint32_t box_rows);
+// Tensor map of packed e2m1 rows (cols a multiple of 128, base 32-byte
+// aligned) whose copies spread 16 codes over 16 bytes of shared memory, as
+// the mixed 8/6/4-bit MMA reads 4-bit operands: boxes of 128 codes (128
+// bytes, 128-byte swizzled) x box_rows.
+cudaError_t make_tmap_e2m1_wide(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols,
+                                uint32_t box_rows);
+
+size_t mx_gemm_scratch_bytes(int S);
+size_t mx_gemm_zero_bytes();
 cudaError_t launch_rmsnorm(const NormLaunch &a, cudaStream_t s);
 cudaError_t launch_mx_quantize(const MxQuantLaunch &a, cudaStream_t s);
 cudaError_t launch_mx_gemm(const MxGemmLaunch &a, cudaStream_t s);

@@ -1,11 +1,47 @@
-// mx_gemm.cu -- products of microscaled rows with 4-bit expert weights:
+// mx_gemm.cu -- products of microscaled rows with 4-bit expert weights, on
+// CTA pairs with block-scaled tensor-core MMAs (tcgen05 .cta_group::2
+// .block_scale):
 //   y[r, n] = sum_k W_e[n, k] x[r, k]                   (moe_mx_product)
 //   h[r, f] = act(W1_e x[r])[f] * (W3_e x[r])[f]        (moe_mx_gated)
-// for every row r of expert e's segment, x in e4m3 or e2m1, W in e2m1, one
-// power-of-two scale per 32 values of K on both sides, sums in fp32.
+// for every row r of expert e's segment, cut into token tiles of near-equal
+// size.  W is e2m1, x e4m3 (kind::mxf8f6f4) or e2m1 (kind::mxf4, twice the
+// rate), one power-of-two scale per 32 values of K on both sides; the tensor
+// cores multiply the scales in and sum in fp32.
+//
+// The weights are the MMA's A operand (M = 256 over the pair), a tile's rows
+// its B operand (N = rows rounded up to 16, half of them in each CTA): a
+// ragged segment costs the MMA columns it needs, and the same kernel streams
+// the weights for a single token.  Each CTA holds 128 weight rows: of the
+// product 128 output columns, of the gated form 64 rows of W1 and the same 64
+// of W3, so that both sums of an output lie in one CTA.
+//
+// Operands reach shared memory as 128-byte rows by TMA: 128 (e4m3) or 256
+// (e2m1) values of K a stage.  Against e4m3 rows the copy spreads 16 weight
+// codes over 16 bytes, the layout of the mixed kind, so HBM and L2 carry 4
+// bits a weight.  Scales are copied 16 to a row (512 values of K, a chunk);
+// four warps move them from shared to tensor memory in the MMA's layout (row
+// r in lane r % 32 of every lane quarter, column r / 32), two chunks deep.
+// The row-major scales of a checkpoint can be used as they are, and rows of x
+// can start at any row: no 128-row tiling of the scales has to fit the
+// segments.
+//
+// Work: a unit is (expert, 256 weight rows, token tile).  Pairs take whole
+// units in turn; what does not fill the last turn is cut along K into equal
+// ranges of chunks, one per pair, where that ends sooner (plan()).  The parts of
+// a cut unit meet in the workspace: each epilogue warp stores its part of the
+// accumulator, and the last of the parts to arrive sums them in K order, so
+// the result does not depend on who was last.
+//
+// Roles per CTA: warp 0 issues the copies, warp 1 of the even CTA the MMAs
+// (two accumulators), warps 4..7 move scales, warps 8..15 drain the
+// accumulator.  All waits are bounded.
+//
+// Method: as gemm_pair.cu; the pages' deployment section (jsqmd.com) asks for
+// quantised experts.
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "internal.h"
@@ -16,148 +52,870 @@ namespace moe {
 
 namespace {
 
+constexpr int kThreads = 512;
+constexpr int kEpiWarps = 8;
+constexpr int kMaxN = 192;               // token rows per tile
+constexpr uint32_t kRowBytes = 128;      // of an operand row in a stage
+constexpr uint32_t kATile = 128 * kRowBytes;
+constexpr int kChunkK = 512;             // values of K per scale chunk (16 scale bytes)
+constexpr int kScSlots = 4;              // scale chunks in shared memory
+constexpr uint32_t kScA = 128 * 16;      // bytes of a chunk's weight scales
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kAccCols = kMaxN;     // accumulators at columns 0 and 192
+constexpr uint32_t kScCol = 2 * kAccCols;  // scale buffers at columns 384 and 448
+constexpr uint32_t kScBuf = 64;          // four words of K: 4 columns of A, 4 unused, 8 of B each
+constexpr int kColChunk = 16;            // accumulator columns per epilogue step
+constexpr uint32_t kXchg = 4 * 2 * 2 * 8 * 32 * 4;  // [warp pair][buf][a|b][8][32] fp32
+constexpr int kMaxPairs = 80;            // pairs a launch may use (74 on 148 SMs)
+constexpr int kParts = 2 * kMaxPairs;    // partial units: two per pair
+constexpr size_t kCounters = static_cast<size_t>(kMaxPairs) * 2 * kEpiWarps;
+
+// Shared memory by the largest token tile: fewer token rows leave room for
+// more stages, which a weight stream needs in flight.
+template <int NMAX>
+struct Smem {
+    static constexpr uint32_t kBTile = NMAX / 2 * kRowBytes;
+    static constexpr uint32_t kStage = kATile + kBTile;
+    static constexpr int kStages = NMAX == 192 ? 6 : NMAX == 96 ? 7 : 9;
+    static constexpr uint32_t kScSlot = kScA + NMAX * 16;
+    static constexpr int kBarriers = 2 * kStages + 2 * kScSlots + 2 * 2 + 2 * 2 + 1 + 8;
+    static constexpr size_t kBytes = 1024 /* alignment slack */ + kStages * kStage +
+                                     kScSlots * kScSlot + kXchg + kBarriers * 8 + 64 +
+                                     2 * (kMaxE + 1) * sizeof(int32_t);
+    static_assert(kBytes <= 227 * 1024, "shared memory");
+    static_assert(kBTile % 1024 == 0, "swizzle atom");
+};
+
 struct GemmParams {
-    int S, K, E, N, act, y_type;
-    const uint8_t *x, *xs, *W1, *s1, *W3, *s3;
-    long long x_stride, xs_stride;
-    const int32_t *offsets;
-    void *y;
-    uint8_t *q, *qs;
+    int S, K, E, N;
+    int rows_blk;            // output columns per unit: 256, or 128 (gated)
+    int act, y_type;
+    const int32_t *offsets;  // [E+1] or nullptr
+    void *y;                 // [S, N] or nullptr
+    uint8_t *q, *qs;         // [S, N] e4m3, [S, qpitch]
+    int qpitch;
+    float *parts;            // [kParts][2 CTAs][part_cols][128 lanes]
+    int part_cols;
+    uint32_t *ctr;           // kCounters, zero before the launch
     uint32_t *err;
 };
 
-constexpr int kTile = 64;
-
-template <int FMT>
-__device__ void load_tile(float (*dst)[33], const uint8_t *q, long long qst, const uint8_t *s,
-                          long long sst, int r0, int rows, int k0)
+// ------------------------------------------------------------------ waiting
+__device__ __forceinline__ bool wait_cl(uint64_t *bar, uint32_t parity,
+                                        volatile uint32_t *abort_flag, uint32_t *gerr,
+                                        uint32_t code)
 {
-    // 64 rows x 32 values: thread t reads eight values of row t / 4.
-    const int r = threadIdx.x >> 2, c = (threadIdx.x & 3) * 8;
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (r0 + r < rows) {
-        const uint8_t *p = q + (r0 + r) * qst;
-        uint2 w;
-        if constexpr (FMT == kMxE4M3) w = *reinterpret_cast<const uint2 *>(p + k0 + c);
-        else w = make_uint2(*reinterpret_cast<const uint32_t *>(p + (k0 + c) / 2), 0u);
-        mx_values8<FMT>(w, s[(r0 + r) * sst + k0 / 32], v);
+    if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
+    const uint64_t t0 = ptx::globaltimer();
+    for (uint32_t it = 1;; ++it) {
+        if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if ((it & 63u) == 0 && ptx::globaltimer() - t0 > kWaitTimeoutNs) {
+            *abort_flag = 1u;
+            if (gerr) atomicOr(gerr, code);
+            return false;
+        }
     }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) dst[r][c + i] = v[i];
 }
 
-template <int FMT, bool GATED>
-__global__ void __launch_bounds__(256) mx_gemm_kernel(const GemmParams p)
+__device__ __forceinline__ bool wait_cl_warp(uint64_t *bar, uint32_t parity,
+                                             volatile uint32_t *abort_flag, uint32_t *gerr,
+                                             uint32_t code)
 {
-    __shared__ float sx[kTile][33], sw[kTile][33], sv[GATED ? kTile : 1][33];
-    __shared__ float sh[GATED ? kTile : 1][kTile + 1];
-    ptx::grid_dep_launch();
-    ptx::grid_dep_wait();
-    const int tid = threadIdx.x;
-    bool bad = false;
-    for (int e = tid; e < p.E; e += 256)
-        if (p.offsets) {
-            const int a = p.offsets[e], b = p.offsets[e + 1];
-            bad |= a < 0 || b < a || b > p.S;
+    const bool ok = wait_cl(bar, parity, abort_flag, gerr, code);
+    const bool all = __all_sync(0xffffffffu, ok);
+    if (!all) *abort_flag = 1u;
+    return all;
+}
+
+__device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity)
+{
+    const uint64_t t0 = ptx::globaltimer();
+    while (!ptx::mbar_try_wait_cluster(bar, parity)) {
+        if (ptx::globaltimer() - t0 > 100000000ull) break;  // 100 ms
+    }
+}
+
+// --------------------------------------------------------------------- work
+__device__ __forceinline__ int ceil16(int v) { return (v + 15) & ~15; }
+
+// A part of a unit: chunks [c0, c1) of K.  When it is not the whole unit, its
+// accumulator goes to slot `part` of the workspace and `first` .. `last` are
+// the pairs that hold the unit's parts, `cut` the unit's number among those
+// that may be cut.
+struct Work {
+    int e, blk, r0, valid, n;
+    int c0, c1;
+    int part, first, last, cut;
+};
+
+// The sequence of work of one pair; every role of both CTAs walks it alike.
+struct Walk {
+    int pair, pairs, units, whole, chunks;   // units [whole, units) may be cut
+    int u;                                   // next whole unit
+    long long it, end, items;                // chunk items of the cut units
+    int first_cut;                           // the first cut unit of this pair
+
+    // Units whole, whole + 1, .. share `items` chunks of K; pair p has
+    // [items p / pairs, items (p + 1) / pairs) of them.
+    __device__ __forceinline__ void start(int pair_, int pairs_, int units_, int whole_, int chunks_)
+    {
+        pair = pair_;
+        pairs = pairs_;
+        units = units_;
+        whole = whole_;
+        chunks = chunks_;
+        u = pair;
+        items = static_cast<long long>(units - whole) * chunks;
+        it = items * pair / pairs;
+        end = items * (pair + 1) / pairs;
+        first_cut = static_cast<int>(it / chunks);
+    }
+
+    __device__ __forceinline__ int owner(long long item) const
+    {
+        return static_cast<int>(((item + 1) * pairs - 1) / items);
+    }
+
+    // Next unit and its chunks; false when the pair is done.
+    __device__ __forceinline__ bool next(Work &w, int &unit)
+    {
+        if (u < whole) {
+            unit = u;
+            u += pairs;
+            w.c0 = 0;
+            w.c1 = chunks;
+            w.part = -1;
+            return true;
         }
-    if (__syncthreads_or(bad)) {
-        if (tid == 0) atomicOr(p.err, kErrOffsets);
+        if (it >= end) return false;
+        const int c = static_cast<int>(it / chunks);
+        const long long base = static_cast<long long>(c) * chunks;
+        unit = whole + c;
+        w.c0 = static_cast<int>(it - base);
+        const long long stop = base + chunks < end ? base + chunks : end;
+        w.c1 = static_cast<int>(stop - base);
+        it = stop;
+        w.part = -1;
+        if (w.c0 != 0 || w.c1 != chunks) {
+            w.cut = c;
+            w.first = owner(base);
+            w.last = owner(base + chunks - 1);
+            w.part = 2 * pair + (c == first_cut ? 0 : 1);
+        }
+        return true;
+    }
+
+    // The slot in which pair p stores its part of cut unit c.
+    __device__ __forceinline__ int part_of(int p, int c) const
+    {
+        return 2 * p + (static_cast<int>((items * p / pairs) / chunks) == c ? 0 : 1);
+    }
+};
+
+// How many of `units` units of `chunks` chunks are taken whole: all of them,
+// or the full turns of the pairs while the rest is cut evenly.  Cutting costs
+// storing, waiting for and summing the parts, about as much as kJoin chunks;
+// it is taken where it saves more than that.
+constexpr int kJoin = 3;
+
+__device__ __forceinline__ int plan(int units, int pairs, int chunks)
+{
+    const int full = units / pairs * pairs;
+    const int rest = units - full;
+    if (rest == 0) return units;
+    const int each = (rest * chunks + pairs - 1) / pairs;
+    return chunks - each > kJoin ? full : units;
+}
+
+template <int NMAX>
+__device__ __forceinline__ int seg_tiles(int cnt) { return (cnt + NMAX - 1) / NMAX; }
+
+// Unit u: expert by the prefix of unit counts, then 256-row block, then tile
+// (neighbouring pairs share weights, and the tiles of an expert stay in L2).
+template <int NMAX>
+__device__ __forceinline__ void place(Work &w, int u, const int32_t *s_off, const int32_t *s_pre,
+                                      int E)
+{
+    int lo = 0, hi = E - 1;
+    while (lo < hi) {  // largest e with pre[e] <= u
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_pre[mid] <= u) lo = mid;
+        else hi = mid - 1;
+    }
+    w.e = lo;
+    const int local = u - s_pre[lo];
+    const int cnt = s_off[lo + 1] - s_off[lo];
+    const int nt = seg_tiles<NMAX>(cnt);
+    const int q = ceil16((cnt + nt - 1) / nt);
+    w.blk = local / nt;
+    const int t = local - w.blk * nt;
+    w.r0 = s_off[lo] + t * q;
+    const int rem = cnt - t * q;
+    w.valid = rem < q ? rem : q;
+    w.n = w.valid > 0 ? ceil16(w.valid) : 16;
+}
+
+__device__ __forceinline__ int warp_scan_incl(int v, int lane)
+{
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const int n = __shfl_up_sync(0xffffffffu, v, off);
+        if (lane >= off) v += n;
+    }
+    return v;
+}
+
+// ----------------------------------------------------------------- epilogue
+// silu(g) * b (act 0) or sigmoid(g) * b (act 1).
+__device__ __forceinline__ float gate_mul(float g, float b, int act)
+{
+    return __fdividef(act ? b : g * b, 1.0f + __expf(-g));
+}
+
+// 16 (bf16) accumulator columns of 32 lanes to rows t0 .. t0+15 of y: lane
+// pairs swap so that each lane stores two neighbouring output columns.
+__device__ __forceinline__ void store_bf16(const GemmParams &p, const float (&v)[16], int row,
+                                           int t0, int valid, int o, int lane)
+{
+    const int odd = lane & 1;
+    __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(p.y) + static_cast<size_t>(row + t0) * p.N + (o & ~1);
+#pragma unroll
+    for (int j = 0; j < 16; j += 2) {
+        const float give = odd ? v[j] : v[j + 1];
+        const float got = __shfl_xor_sync(0xffffffffu, give, 1);
+        const __nv_bfloat162 b = odd ? __floats2bfloat162_rn(got, v[j + 1])
+                                     : __floats2bfloat162_rn(v[j], got);
+        if (o < p.N && t0 + j + odd < valid)
+            *reinterpret_cast<__nv_bfloat162 *>(y + static_cast<size_t>(j + odd) * p.N) = b;
+    }
+}
+
+__device__ __forceinline__ void store_fp32(const GemmParams &p, const float (&v)[16], int row,
+                                           int t0, int valid, int o)
+{
+    float *y = static_cast<float *>(p.y) + static_cast<size_t>(row + t0) * p.N + o;
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+        if (o < p.N && t0 + j < valid) y[static_cast<size_t>(j) * p.N] = v[j];
+}
+
+// Eight tokens of h at 32 columns f (one per lane): bf16, or e4m3 with the
+// scale of the 32 lanes.
+__device__ __forceinline__ void store_h8(const GemmParams &p, const float (&v)[8], int row, int t0,
+                                         int valid, int f, int lane)
+{
+    if (p.y != nullptr) {
+        const int odd = lane & 1;
+        __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(p.y) + static_cast<size_t>(row + t0) * p.N + (f & ~1);
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            const float give = odd ? v[j] : v[j + 1];
+            const float got = __shfl_xor_sync(0xffffffffu, give, 1);
+            const __nv_bfloat162 b = odd ? __floats2bfloat162_rn(got, v[j + 1])
+                                         : __floats2bfloat162_rn(v[j], got);
+            if (t0 + j + odd < valid)
+                *reinterpret_cast<__nv_bfloat162 *>(y + static_cast<size_t>(j + odd) * p.N) = b;
+        }
         return;
     }
-    const int e = blockIdx.y, n0 = blockIdx.x * kTile;
-    const int first = p.offsets ? p.offsets[e] : 0, last = p.offsets ? p.offsets[e + 1] : p.S;
-    const size_t wrow = static_cast<size_t>(e) * p.N;
-    const int wp = p.K / 2, sp = mx_scale_pitch(p.K);
-    const uint8_t *W1 = p.W1 + wrow * wp, *s1 = p.s1 + wrow * sp;
-    const uint8_t *W3 = GATED ? p.W3 + wrow * wp : nullptr, *s3 = GATED ? p.s3 + wrow * sp : nullptr;
-    const int tr = tid >> 4, tc = tid & 15;
-    for (int r0 = first; r0 < last; r0 += kTile) {
-        float a[4][4] = {}, b[4][4] = {};
-        for (int k0 = 0; k0 < p.K; k0 += 32) {
-            load_tile<FMT>(sx, p.x, p.x_stride, p.xs, p.xs_stride, r0, last, k0);
-            load_tile<kMxE2M1>(sw, W1, wp, s1, sp, n0, p.N, k0);
-            if constexpr (GATED) load_tile<kMxE2M1>(sv, W3, wp, s3, sp, n0, p.N, k0);
-            __syncthreads();
-            for (int k = 0; k < 32; ++k)
-                for (int i = 0; i < 4; ++i)
-                    for (int j = 0; j < 4; ++j) {
-                        a[i][j] = fmaf(sx[tr + 16 * i][k], sw[tc + 16 * j][k], a[i][j]);
-                        if constexpr (GATED) b[i][j] = fmaf(sx[tr + 16 * i][k], sv[tc + 16 * j][k], b[i][j]);
-                    }
-            __syncthreads();
-        }
-        for (int i = 0; i < 4; ++i)
-            for (int j = 0; j < 4; ++j) {
-                const int r = r0 + tr + 16 * i, n = n0 + tc + 16 * j;
-                float v = a[i][j];
-                if constexpr (GATED) {
-                    const float g = v;
-                    v = (p.act ? 1.0f : g) * b[i][j] / (1.0f + expf(-g));
-                    sh[tr + 16 * i][tc + 16 * j] = v;
-                }
-                if (p.y && r < last && n < p.N) {
-                    const size_t at = static_cast<size_t>(r) * p.N + n;
-                    if (p.y_type == kTypeBf16) static_cast<__nv_bfloat16 *>(p.y)[at] = __float2bfloat16_rn(v);
-                    else static_cast<float *>(p.y)[at] = v;
-                }
-            }
-        if constexpr (GATED) {
-            __syncthreads();
-            const int r = r0 + (tid >> 2), c = (tid & 3) * 16;
-            if (p.q) {
-                // two threads a block of 32 columns, sixteen values each
-                uint32_t m = 0;
-                for (int i = 0; i < 16; ++i) m = max(m, abs_bits(sh[tid >> 2][c + i]));
-                m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-                const uint32_t code = mx_scale_code<kMxE4M3>(m);
-                if (r < last && n0 + c < p.N) {
-                    for (int o = 0; o < 16; o += 8) {
-                        float v[8];
-                        for (int i = 0; i < 8; ++i) v[i] = sh[tid >> 2][c + o + i];
-                        *reinterpret_cast<uint2 *>(p.q + static_cast<size_t>(r) * p.N + n0 + c + o) =
-                            mx_codes8<kMxE4M3>(v, code);
-                    }
-                    uint8_t *s = p.qs + static_cast<size_t>(r) * mx_scale_pitch(p.N);
-                    if ((tid & 1) == 0) s[(n0 + c) / 32] = static_cast<uint8_t>(code);
-                    if (n0 + c + 16 == p.N)
-                        for (int b = p.N / 32; b < mx_scale_pitch(p.N); ++b) s[b] = 0;
-                }
-            }
-            __syncthreads();
-        }
+    uint32_t mine = 0;       // the scale byte of token t0 + lane
+    uint32_t w[2] = {0u, 0u};  // this lane's codes of tokens 0..3 and 4..7
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t c = mx_scale_code<kMxE4M3>(__reduce_max_sync(0xffffffffu, abs_bits(v[j])));
+        if (lane == j) mine = c;
+        const uint32_t code =
+            c == 255u ? 0u : __nv_cvt_float_to_fp8(v[j] * mx_inv_scale(c), __NV_SATFINITE, __NV_E4M3);
+        w[j >> 2] |= code << (8 * (j & 3));
+    }
+    if (lane < 8 && t0 + lane < valid) {
+        uint8_t *s = p.qs + static_cast<size_t>(row + t0 + lane) * p.qpitch;
+        s[f >> 5] = static_cast<uint8_t>(mine);
+        if ((f >> 5) == (p.N >> 5) - 1)
+            for (int b = p.N >> 5; b < p.qpitch; ++b) s[b] = 0;
+    }
+    // 4 x 4 bytes transposed over groups of four lanes: lane 4i + t gets the
+    // codes of columns 4i .. 4i+3 of token t.
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        uint32_t a = w[g];
+        uint32_t b = __shfl_xor_sync(0xffffffffu, a, 1);
+        a = (lane & 1) ? __byte_perm(a, b, 0x3715) : __byte_perm(a, b, 0x6240);
+        b = __shfl_xor_sync(0xffffffffu, a, 2);
+        a = (lane & 2) ? __byte_perm(a, b, 0x3276) : __byte_perm(a, b, 0x5410);
+        const int t = t0 + 4 * g + (lane & 3);
+        if (t < valid)
+            *reinterpret_cast<uint32_t *>(p.q + static_cast<size_t>(row + t) * p.N + (f & ~3)) = a;
     }
 }
 
-}  // namespace
-
-size_t mx_gemm_zero_bytes(int, int, int) { return 0; }
-size_t mx_gemm_scratch_bytes(int, int, int) { return 0; }
-
-cudaError_t launch_mx_gemm(const MxGemmLaunch &a, cudaStream_t s)
+// ------------------------------------------------------------------- kernel
+template <int FMT, bool GATED, int NMAX>
+__global__ void __launch_bounds__(kThreads, 1)
+    mx_pair_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ CUtensorMap tmW3,
+                   const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmS1,
+                   const __grid_constant__ CUtensorMap tmS3, const __grid_constant__ CUtensorMap tmXs,
+                   const GemmParams p)
 {
+    using SM = Smem<NMAX>;
+    constexpr int kStages = SM::kStages;
+    constexpr int kStageK = FMT == kMxE4M3 ? 128 : 256;      // values of K per stage
+    constexpr int kStagesPerChunk = kChunkK / kStageK;
+    // Bytes a CTA's copies count per stage: a spread copy counts the 4-bit
+    // codes it moves, not the shared memory it covers.
+    constexpr uint32_t kStageTx = SM::kBTile + (FMT == kMxE4M3 ? kATile / 2 : kATile);
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                                ~static_cast<uintptr_t>(1023));
+    const int warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31;
+    const uint32_t cta = ptx::cluster_ctarank();  // 0: issues the MMAs
+    const bool leader = (cta == 0);
+
+    uint8_t *scales = smem + kStages * SM::kStage;
+    float *xchg = reinterpret_cast<float *>(scales + kScSlots * SM::kScSlot);
+    uint64_t *full = reinterpret_cast<uint64_t *>(reinterpret_cast<uint8_t *>(xchg) + kXchg);
+    uint64_t *empty = full + kStages;
+    uint64_t *cfull = empty + kStages;      // [kScSlots] scale chunk in shared memory
+    uint64_t *cempty = cfull + kScSlots;    // [kScSlots]
+    uint64_t *tfull = cempty + kScSlots;    // [2] accumulator
+    uint64_t *tempty = tfull + 2;           // [2]
+    uint64_t *sfull = tempty + 2;           // [2] scale chunk in tensor memory
+    uint64_t *sempty = sfull + 2;           // [2]
+    uint64_t *drain = sempty + 2;           // [1]
+    uint64_t *xbar = drain + 1;             // [4 warp pairs][2 exchange buffers]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(xbar + 8);
+    volatile uint32_t *abort_flag = tmem_slot + 1;
+    int32_t *s_off = reinterpret_cast<int32_t *>(tmem_slot + 16);
+    int32_t *s_pre = s_off + (kMaxE + 1);
+
+    const int E = p.offsets ? p.E : 1;
+    const int blocks = (p.N + p.rows_blk - 1) / p.rows_blk;
+    const int chunks = (p.K + kChunkK - 1) / kChunkK;
+    const int ksteps = (p.K + kStageK - 1) / kStageK;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            ptx::mbar_init(&full[s], 1);
+            ptx::mbar_init(&empty[s], 1);
+        }
+        for (int s = 0; s < kScSlots; ++s) {
+            ptx::mbar_init(&cfull[s], 1);
+            ptx::mbar_init(&cempty[s], 4);
+        }
+        for (int b = 0; b < 2; ++b) {
+            ptx::mbar_init(&tfull[b], 1);
+            ptx::mbar_init(&tempty[b], 2 * kEpiWarps);
+            ptx::mbar_init(&sfull[b], 8);
+            ptx::mbar_init(&sempty[b], 1);
+        }
+        ptx::mbar_init(drain, 1);
+        for (int b = 0; b < 8; ++b) ptx::mbar_init(&xbar[b], 64);
+        *abort_flag = 0u;
+        ptx::fence_barrier_init();
+    }
+    if (threadIdx.x == 32) {
+        ptx::prefetch_tensormap(&tmW1);
+        ptx::prefetch_tensormap(&tmX);
+        ptx::prefetch_tensormap(&tmS1);
+        ptx::prefetch_tensormap(&tmXs);
+        if (GATED) {
+            ptx::prefetch_tensormap(&tmW3);
+            ptx::prefetch_tensormap(&tmS3);
+        }
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc_pair(tmem_slot, kTmemCols);
+        ptx::tmem_relinquish_pair();
+    }
+    // Everything above overlaps the previous kernel; from here on its results
+    // are read.
+    ptx::grid_dep_wait();
+    if (warp == 2) {
+        // Segment table and the prefix of unit counts per expert.
+        const int per = (E + 31) >> 5;
+        const int base = lane * per;
+        bool bad = false;
+        int nu = 0;
+        for (int i = 0; i < per; ++i) {
+            const int e = base + i;
+            if (e < E) {
+                const int o0 = p.offsets ? p.offsets[e] : 0;
+                const int o1 = p.offsets ? p.offsets[e + 1] : p.S;
+                s_off[e] = o0;
+                if (e == E - 1) s_off[E] = o1;
+                if (o0 < 0 || o1 < o0 || o1 > p.S) bad = true;
+                else nu += seg_tiles<NMAX>(o1 - o0) * blocks;
+            }
+        }
+        __syncwarp();
+        bad = __any_sync(0xffffffffu, bad);
+        if (bad) {
+            nu = 0;
+            if (lane == 0 && leader) atomicOr(p.err, kErrOffsets);
+        }
+        const int incl = warp_scan_incl(nu, lane);
+        int run = incl - nu;
+        for (int i = 0; i < per; ++i) {
+            const int e = base + i;
+            if (e < E) {
+                s_pre[e] = run;
+                if (!bad) run += seg_tiles<NMAX>(s_off[e + 1] - s_off[e]) * blocks;
+            }
+        }
+        if (lane == 31) s_pre[E] = incl;
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    // Both CTAs' barriers are initialised before either CTA signals the other.
+    ptx::cluster_sync();
+    ptx::tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    const int units = s_pre[E];
+    const int pairs = static_cast<int>(gridDim.x >> 1);
+    const int whole = plan(units, pairs, chunks);
+    Walk walk;
+    walk.start(static_cast<int>(blockIdx.x >> 1), pairs, units, whole, chunks);
+
+    // Shared::cluster addresses of the even CTA's barriers.
+    const uint32_t full0 = ptx::mapa_shared(ptx::smem_addr(full), 0);
+    const uint32_t tempty0 = ptx::mapa_shared(ptx::smem_addr(tempty), 0);
+    const uint32_t sfull0 = ptx::mapa_shared(ptx::smem_addr(sfull), 0);
+
+    Work w;
+    int unit;
+    if (warp == 0) {
+        if (lane == 0) {
+            uint32_t stage = 0, phase = 0, issued = 0;
+            uint32_t slot = 0, cphase = 0, cissued = 0;
+            uint32_t last_parity[kStages], clast[kScSlots];
+#pragma unroll
+            for (int s = 0; s < kStages; ++s) last_parity[s] = 0;
+#pragma unroll
+            for (int s = 0; s < kScSlots; ++s) clast[s] = 0;
+            const uint64_t pol = ptx::policy_evict_normal();
+            bool stop = false;
+            while (!stop && walk.next(w, unit)) {
+                place<NMAX>(w, unit, s_off, s_pre, E);
+                const int arow = w.e * p.N + w.blk * p.rows_blk + static_cast<int>(cta) * (p.rows_blk / 2);
+                const int brow = w.r0 + static_cast<int>(cta) * (w.n >> 1);
+                for (int c = w.c0; c < w.c1 && !stop; ++c) {
+                    if (!wait_cl(&cempty[slot], cphase ^ 1u, abort_flag, p.err, kErrTimeoutTma)) {
+                        stop = true;
+                        break;
+                    }
+                    uint8_t *sc = scales + slot * SM::kScSlot;
+                    ptx::mbar_arrive_expect_tx(&cfull[slot], SM::kScSlot);
+                    ptx::tma_load_2d(sc, &tmS1, &cfull[slot], c * 16, arow);
+                    if (GATED) ptx::tma_load_2d(sc + kScA / 2, &tmS3, &cfull[slot], c * 16, arow);
+                    ptx::tma_load_2d(sc + kScA, &tmXs, &cfull[slot], c * 16, w.r0);
+                    cissued |= 1u << slot;
+                    clast[slot] = cphase;
+                    if (++slot == kScSlots) {
+                        slot = 0;
+                        cphase ^= 1u;
+                    }
+                    for (int i = 0; i < kStagesPerChunk; ++i) {
+                        const int ks = c * kStagesPerChunk + i;
+                        if (ks >= ksteps) break;
+                        if (!wait_cl(&empty[stage], phase ^ 1u, abort_flag, p.err, kErrTimeoutMma)) {
+                            stop = true;
+                            break;
+                        }
+                        uint8_t *sa = smem + stage * SM::kStage;
+                        const uint32_t fb = full0 + 8 * stage;
+                        if (leader) ptx::mbar_arrive_expect_tx(&full[stage], 2 * kStageTx);
+                        // 128 bytes of a row in shared memory: the coordinate
+                        // counts codes (the spread copy) or bytes
+                        ptx::tma_load_2d_pair(sa, &tmW1, fb, ks * 128, arow, pol);
+                        if (GATED) ptx::tma_load_2d_pair(sa + kATile / 2, &tmW3, fb, ks * 128, arow, pol);
+                        ptx::tma_load_2d_pair(sa + kATile, &tmX, fb, ks * 128, brow, pol);
+                        issued |= 1u << stage;
+                        last_parity[stage] = phase;
+                        if (++stage == static_cast<uint32_t>(kStages)) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                }
+            }
+            // No copy may still be landing in shared memory at exit.  The odd
+            // CTA's operand copies count on the even CTA's barriers, and the
+            // final cluster barrier orders its exit after this.
+            if (leader)
+                for (int s = 0; s < kStages; ++s)
+                    if (issued & (1u << s)) drain_wait(&full[s], last_parity[s]);
+            for (int s = 0; s < kScSlots; ++s)
+                if (cissued & (1u << s)) drain_wait(&cfull[s], clast[s]);
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {
+            uint32_t stage = 0, phase = 0, sc = 0;
+            bool stop = false;
+            for (uint32_t i = 0; !stop && walk.next(w, unit); ++i) {
+                place<NMAX>(w, unit, s_off, s_pre, E);
+                const uint32_t buf = i & 1u;
+                if (!wait_cl(&tempty[buf], ((i >> 1) & 1u) ^ 1u, abort_flag, p.err, kErrTimeoutEpi))
+                    break;
+                ptx::tc_fence_after();
+                const uint32_t dacc = tmem + buf * kAccCols;
+                uint32_t acc = 0;
+                for (int c = w.c0; c < w.c1 && !stop; ++c, ++sc) {
+                    const uint32_t sb = sc & 1u;
+                    if (!wait_cl(&sfull[sb], (sc >> 1) & 1u, abort_flag, p.err, kErrTimeoutTma)) {
+                        stop = true;
+                        break;
+                    }
+                    ptx::tc_fence_after();
+                    const uint32_t scol = tmem + kScCol + sb * kScBuf;
+                    for (int j = 0; j < kStagesPerChunk; ++j) {
+                        const int ks = c * kStagesPerChunk + j;
+                        if (ks >= ksteps) break;
+                        if (!wait_cl(&full[stage], phase, abort_flag, p.err, kErrTimeoutTma)) {
+                            stop = true;
+                            break;
+                        }
+                        ptx::tc_fence_after();
+                        const uint32_t sa = ptx::smem_addr(smem + stage * SM::kStage);
+                        const uint32_t sx = sa + kATile;
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk) {
+                            const uint64_t da = ptx::sw128_kmajor_desc(sa + kk * 32);
+                            const uint64_t db = ptx::sw128_kmajor_desc(sx + kk * 32);
+                            if constexpr (FMT == kMxE4M3) {
+                                const uint32_t word = scol + 16 * j;  // 4 scales of 32: byte kk
+                                ptx::tc_mma_mxf8f6f4_pair(
+                                    dacc, da, db,
+                                    ptx::idesc_mx(256, w.n, ptx::kMxf8f6f4E2M1, ptx::kMxf8f6f4E4M3, kk),
+                                    word, word + 8, acc);
+                            } else {
+                                // a stage may end after its first 128 values
+                                if (kk >= 2 && ks * kStageK + 128 >= p.K) break;
+                                const uint32_t word = scol + 16 * (2 * j + (kk >> 1));
+                                ptx::tc_mma_mxf4_pair(
+                                    dacc, da, db,
+                                    ptx::idesc_mx(256, w.n, ptx::kMxf4E2M1, ptx::kMxf4E2M1, 2 * (kk & 1)),
+                                    word, word + 8, acc);
+                            }
+                            acc = 1;
+                        }
+                        ptx::tc_commit_pair(&empty[stage], 0x3);
+                        if (++stage == static_cast<uint32_t>(kStages)) {
+                            stage = 0;
+                            phase ^= 1u;
+                        }
+                    }
+                    if (!stop) ptx::tc_commit_pair(&sempty[sb], 0x3);
+                }
+                if (!stop) ptx::tc_commit_pair(&tfull[buf], 0x3);
+            }
+            // Every MMA issued above has finished once this arrives.
+            ptx::tc_commit_pair(drain, 0x1);
+            drain_wait(drain, 0u);
+        }
+    } else if (warp >= 4 && warp < 8) {
+        // Scales: shared memory (row-major, 16 bytes a row) to this warp's
+        // lane quarter of tensor memory.
+        const uint32_t tq = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + kScCol;
+        uint32_t slot = 0, cphase = 0, sc = 0;
+        bool stop = false;
+        while (!stop && walk.next(w, unit)) {
+            place<NMAX>(w, unit, s_off, s_pre, E);
+            for (int c = w.c0; c < w.c1; ++c, ++sc) {
+                if (!wait_cl_warp(&cfull[slot], cphase, abort_flag, p.err, kErrTimeoutTma)) {
+                    stop = true;
+                    break;
+                }
+                constexpr int kB = NMAX / 32;
+                const uint4 *src = reinterpret_cast<const uint4 *>(scales + slot * SM::kScSlot);
+                uint4 a[4], b[kB];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) a[i] = src[32 * i + lane];
+#pragma unroll
+                for (int i = 0; i < kB; ++i) b[i] = src[128 + 32 * i + lane];
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&cempty[slot]);
+                if (++slot == kScSlots) {
+                    slot = 0;
+                    cphase ^= 1u;
+                }
+                const uint32_t sb = sc & 1u;
+                if (!wait_cl_warp(&sempty[sb], ((sc >> 1) & 1u) ^ 1u, abort_flag, p.err, kErrTimeoutMma)) {
+                    stop = true;
+                    break;
+                }
+                ptx::tc_fence_after();
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t r[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        r[i] = 0u;
+                        if (i < 4) r[i] = reinterpret_cast<const uint32_t *>(&a[i])[j];
+                        if (i >= 8 && i - 8 < kB) r[i] = reinterpret_cast<const uint32_t *>(&b[i - 8])[j];
+                    }
+                    ptx::tmem_st16(tq + sb * kScBuf + 16 * j, r);
+                }
+                ptx::tc_wait_st();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive_cluster(sfull0 + 8 * sb);
+            }
+        }
+    } else if (warp >= 8) {
+        // Epilogue: warp w reads tensor-memory lanes 32*(w%4)..+31; the two
+        // warps of a lane quarter take alternate chunks of 16 columns.
+        const int q = warp & 3;
+        const int half = (warp - 8) >> 2;
+        const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
+        const int wpair = (q & 1) + 2 * half;  // (a, b) warp pairs: quarters (0,2) and (1,3)
+        const bool is_a = q < 2;               // lanes 0..63: W1 products (gated)
+        float *xa = xchg + wpair * (2 * 2 * 8 * 32);
+        uint32_t xuse[2] = {0u, 0u};
+        int xb = 0;
+        bool stop = false;
+        for (uint32_t i = 0; !stop && walk.next(w, unit); ++i) {
+            place<NMAX>(w, unit, s_off, s_pre, E);
+            const uint32_t buf = i & 1u;
+            if (!wait_cl_warp(&tfull[buf], (i >> 1) & 1u, abort_flag, p.err, kErrTimeoutMma)) break;
+            ptx::tc_fence_after();
+            const uint32_t tb = tmem + lane_base + buf * kAccCols;
+            const int nch = w.n / kColChunk;
+            // output column of this lane: product, or h of the lane's quarter
+            const int o = GATED ? w.blk * 128 + static_cast<int>(cta) * 64 + (q & 1) * 32 + lane
+                                : w.blk * 256 + static_cast<int>(cta) * 128 + 32 * q + lane;
+            const size_t pstep = static_cast<size_t>(p.part_cols) * 128;  // one CTA's part
+            if (w.part >= 0) {
+                float *dst = p.parts + (static_cast<size_t>(w.part) * 2 + cta) * pstep + 32 * q + lane;
+                for (int c = half; c < nch; c += 2) {
+                    uint32_t r[16];
+                    ptx::tmem_ld16(tb + static_cast<uint32_t>(c * kColChunk), r);
+                    ptx::tc_wait_ld();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        __stcg(dst + static_cast<size_t>(c * kColChunk + j) * 128, __uint_as_float(r[j]));
+                }
+            } else {
+                for (int c = half; c < nch; c += 2) {
+                    uint32_t r[16];
+                    ptx::tmem_ld16(tb + static_cast<uint32_t>(c * kColChunk), r);
+                    ptx::tc_wait_ld();
+                    if constexpr (GATED) {
+                        // a warps keep tokens 0..7 of the chunk and hand 8..15
+                        // to their b partner; b warps the other way round.
+                        float *mine = xa + xb * (2 * 8 * 32) + (is_a ? 0 : 8 * 32);
+                        float *theirs = xa + xb * (2 * 8 * 32) + (is_a ? 8 * 32 : 0);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            mine[j * 32 + lane] = __uint_as_float(r[is_a ? 8 + j : j]);
+                        ptx::mbar_arrive(&xbar[wpair * 2 + xb]);
+                        const bool okx = bounded_wait(&xbar[wpair * 2 + xb], xuse[xb] & 1u, abort_flag,
+                                                      p.err, kErrTimeoutEpi);
+                        ++xuse[xb];
+                        if (!__all_sync(0xffffffffu, okx)) {
+                            stop = true;
+                            break;
+                        }
+                        float v[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float ot = theirs[j * 32 + lane];
+                            const float g = is_a ? __uint_as_float(r[j]) : ot;
+                            const float b = is_a ? ot : __uint_as_float(r[8 + j]);
+                            v[j] = gate_mul(g, b, p.act);
+                        }
+                        store_h8(p, v, w.r0, c * kColChunk + (is_a ? 0 : 8), w.valid, o, lane);
+                        xb ^= 1;
+                    } else {
+                        float v[16];
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
+                        if (p.y_type == kTypeBf16) store_bf16(p, v, w.r0, c * kColChunk, w.valid, o, lane);
+                        else store_fp32(p, v, w.r0, c * kColChunk, w.valid, o);
+                    }
+                }
+                if (stop) break;
+            }
+            // The accumulator may be reused once every epilogue warp of both
+            // CTAs has read it.
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (leader) ptx::mbar_arrive(&tempty[buf]);
+                else ptx::mbar_arrive_cluster(tempty0 + 8 * buf);
+            }
+            if (w.part >= 0) {
+                // The last warp to arrive (of the warp's own columns and
+                // lanes; gated: of the pair of warps with both sums) adds the
+                // parts in K order.
+                __threadfence();
+                __syncwarp();
+                uint32_t seen = 0;
+                uint32_t *ctr = p.ctr + (static_cast<size_t>(w.cut) * 2 + cta) * kEpiWarps +
+                                (GATED ? wpair : warp - 8);
+                if (lane == 0) seen = atomicAdd(ctr, 1u);
+                seen = __shfl_sync(0xffffffffu, seen, 0);
+                const uint32_t all = static_cast<uint32_t>(w.last - w.first + 1) * (GATED ? 2u : 1u);
+                if (seen + 1 == all) {
+                    __threadfence();
+                    for (int c = half; c < nch; c += 2) {
+#pragma unroll
+                        for (int h8 = 0; h8 < 16; h8 += 8) {
+                            float v[8], u[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) v[j] = u[j] = 0.0f;
+                            for (int pr = w.first; pr <= w.last; ++pr) {
+                                const float *src =
+                                    p.parts + (static_cast<size_t>(walk.part_of(pr, w.cut)) * 2 + cta) * pstep +
+                                    static_cast<size_t>(c * kColChunk + h8) * 128 + lane + 32 * (GATED ? (q & 1) : q);
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) {
+                                    v[j] += __ldcg(src + j * 128);
+                                    if (GATED) u[j] += __ldcg(src + j * 128 + 64);
+                                }
+                            }
+                            if constexpr (GATED) {
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) v[j] = gate_mul(v[j], u[j], p.act);
+                                store_h8(p, v, w.r0, c * kColChunk + h8, w.valid, o, lane);
+                            } else {
+                                // rows of this half chunk through the common stores
+                                float z[16];
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) z[j] = j < 8 ? v[j] : 0.0f;
+                                const int t0 = c * kColChunk + h8;
+                                const int lim = t0 + 8 < w.valid ? t0 + 8 : w.valid;
+                                if (p.y_type == kTypeBf16) store_bf16(p, z, w.r0, t0, lim, o, lane);
+                                else store_fp32(p, z, w.r0, t0, lim, o);
+                            }
+                        }
+                    }
+                }
+            }
+        }
+    }
+
+    ptx::grid_dep_launch();
+    ptx::tc_fence_before();
+    __syncthreads();
+    // Neither CTA may free tensor memory or exit while the other still
+    // signals its barriers or reads the accumulators.
+    ptx::cluster_sync();
+    if (warp == 1) {
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc_pair(tmem, kTmemCols);
+    }
+    ptx::cluster_sync();
+}
+
+// Clusters of two that fit the device at a time, per kernel.
+template <int FMT, bool GATED, int NMAX>
+int pair_count(cudaLaunchConfig_t &cfg)
+{
+    static std::atomic<int> known[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
+    int n = known[dev].load(std::memory_order_relaxed);
+    if (n > 0) return n;
+    if (cudaOccupancyMaxActiveClusters(&n, mx_pair_kernel<FMT, GATED, NMAX>, &cfg) != cudaSuccess || n < 1)
+        n = device_sm_count() / 2;
+    n = std::max(1, std::min(n, kMaxPairs));
+    known[dev].store(n, std::memory_order_relaxed);
+    return n;
+}
+
+int part_cols(int S) { return std::min(kMaxN, (S + 15) / 16 * 16); }
+
+template <int FMT, bool GATED, int NMAX>
+cudaError_t launch_t(const MxGemmLaunch &a, cudaStream_t s)
+{
+    using SM = Smem<NMAX>;
+    const uint64_t wrows = static_cast<uint64_t>(a.E) * a.N;
+    const uint32_t abox = GATED ? 64 : 128;
+    const int xbytes = FMT == kMxE4M3 ? a.K : a.K / 2;
+    const int nsc = a.K / kMxBlock, wsc = mx_scale_pitch(a.K);
+    CUtensorMap tW1, tW3, tX, tS1, tS3, tXs;
+    auto weights = [&](CUtensorMap *m, const uint8_t *w) {
+        return FMT == kMxE4M3 ? make_tmap_e2m1_wide(m, w, wrows, a.K, abox)
+                              : make_tmap_rows(m, w, wrows, a.K / 2, a.K / 2, 128, abox);
+    };
+    cudaError_t e = weights(&tW1, a.W1);
+    if (e == cudaSuccess) e = make_tmap_rows(&tS1, a.s1, wrows, nsc, wsc, 16, abox);
+    if (GATED) {
+        if (e == cudaSuccess) e = weights(&tW3, a.W3);
+        if (e == cudaSuccess) e = make_tmap_rows(&tS3, a.s3, wrows, nsc, wsc, 16, abox);
+    } else {
+        tW3 = tW1;
+        tS3 = tS1;
+    }
+    if (e == cudaSuccess) e = make_tmap_rows(&tX, a.x, a.S, xbytes, a.x_stride, 128, NMAX / 2);
+    if (e == cudaSuccess) e = make_tmap_rows(&tXs, a.xs, a.S, nsc, a.xs_stride, 16, NMAX);
+    if (e != cudaSuccess) return e;
+    auto *kernel = mx_pair_kernel<FMT, GATED, NMAX>;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(SM::kBytes));
+    if (e != cudaSuccess) return e;
+
     GemmParams p{};
     p.S = a.S;
     p.K = a.K;
     p.E = a.E;
     p.N = a.N;
+    p.rows_blk = GATED ? 128 : 256;
     p.act = a.act;
     p.y_type = a.y_type;
-    p.x = a.x;
-    p.xs = a.xs;
-    p.x_stride = a.x_stride;
-    p.xs_stride = a.xs_stride;
-    p.W1 = a.W1;
-    p.s1 = a.s1;
-    p.W3 = a.W3;
-    p.s3 = a.s3;
     p.offsets = a.offsets;
     p.y = a.y;
     p.q = a.q;
     p.qs = a.qs;
+    p.qpitch = mx_scale_pitch(a.N);
+    p.ctr = reinterpret_cast<uint32_t *>(a.counters);
+    p.parts = reinterpret_cast<float *>(a.scratch);
+    p.part_cols = part_cols(a.S);
     p.err = a.err;
-    auto *k = a.fmt == kMxE4M3 ? (a.W3 ? mx_gemm_kernel<kMxE4M3, true> : mx_gemm_kernel<kMxE4M3, false>)
-                               : (a.W3 ? mx_gemm_kernel<kMxE2M1, true> : mx_gemm_kernel<kMxE2M1, false>);
-    return launch_pdl(k, dim3((a.N + kTile - 1) / kTile, a.E), dim3(256), 0, s, a.pdl, p);
+
+    cudaLaunchConfig_t cfg = {};
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = SM::kBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    cfg.gridDim = dim3(2);
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * pair_count<FMT, GATED, NMAX>(cfg)));
+    cfg.numAttrs = a.pdl ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, tW1, tW3, tX, tS1, tS3, tXs, p);
+}
+
+template <int FMT, bool GATED>
+cudaError_t launch_n(const MxGemmLaunch &a, cudaStream_t s)
+{
+    const int rows = (a.S + a.E - 1) / a.E;  // per expert, when they are even
+    if (rows <= 24) return launch_t<FMT, GATED, 32>(a, s);
+    if (rows <= 72) return launch_t<FMT, GATED, 96>(a, s);
+    return launch_t<FMT, GATED, 192>(a, s);
+}
+
+}  // namespace
+
+size_t mx_gemm_zero_bytes() { return kCounters * sizeof(uint32_t); }
+
+size_t mx_gemm_scratch_bytes(int S)
+{
+    return static_cast<size_t>(kParts) * 2 * 128 * part_cols(S) * sizeof(float);
+}
+
+cudaError_t launch_mx_gemm(const MxGemmLaunch &a, cudaStream_t s)
+{
+    if (a.fmt == kMxE4M3) return a.W3 ? launch_n<kMxE4M3, true>(a, s) : launch_n<kMxE4M3, false>(a, s);
+    return a.W3 ? launch_n<kMxE2M1, true>(a, s) : launch_n<kMxE2M1, false>(a, s);
 }
 
 }  // namespace moe

@@ -409,6 +409,56 @@ __device__ __forceinline__ void tc_mma_bf16_pair(uint32_t d_tmem, uint64_t adesc
         : "memory");
 }
 
+// Block-scaled pair MMAs: D (+)= (A sA) (B sB)^T, one power-of-two scale per
+// 32 K elements of each row of A and B, read from tensor memory: row r of a
+// scale operand lies in lane r % 32 (the same in all four lane quarters) of
+// column r / 32, and the byte of that column's word is selected by the
+// instruction descriptor.  A's scales cover the CTA's own 128 rows, B's all N
+// columns of D in both CTAs.
+// A e2m1 (in 16-byte groups of 16 codes), B e4m3, K = 32: one scale a row.
+__device__ __forceinline__ void tc_mma_mxf8f6f4_pair(uint32_t d_tmem, uint64_t adesc,
+                                                     uint64_t bdesc, uint32_t idesc,
+                                                     uint32_t sfa, uint32_t sfb,
+                                                     uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf8f6f4.block_scale.scale_vec::1X"
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// A and B e2m1 (packed), K = 64: two scales a row, in consecutive bytes.
+__device__ __forceinline__ void tc_mma_mxf4_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                                 uint32_t idesc, uint32_t sfa, uint32_t sfb,
+                                                 uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X"
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// Instruction descriptor of the block-scaled kinds with power-of-two (E8M0)
+// scales, both operands K-major: `a` and `b` are the kind's format codes,
+// `sf` the first byte of the scale words to use.
+__device__ __forceinline__ uint32_t idesc_mx(int M, int N, uint32_t a, uint32_t b, uint32_t sf)
+{
+    return (sf << 4)                                   // byte of B's scale words
+           | (a << 7)                                  // A format
+           | (b << 10)                                 // B format
+           | (static_cast<uint32_t>(N >> 3) << 17)     // N / 8
+           | (1u << 23)                                // scales E8M0
+           | (static_cast<uint32_t>(M >> 4) << 24)     // M / 16
+           | (sf << 29);                               // byte of A's scale words
+}
+constexpr uint32_t kMxf8f6f4E4M3 = 0, kMxf8f6f4E2M1 = 5, kMxf4E2M1 = 1;
+
 // Arrive once on the mbarrier at the same offset in each CTA of `cta_mask`
 // when the pair MMAs this thread issued so far have completed.
 __device__ __forceinline__ void tc_commit_pair(uint64_t *bar, uint16_t cta_mask)
