@@ -34,7 +34,8 @@
 //
 // Roles per CTA: warp 0 issues the copies, warp 1 of the even CTA the MMAs
 // (two accumulators), warps 4..7 move scales, warps 8..15 drain the
-// accumulator.  All waits are bounded.
+// accumulator; warp 2 decodes units ahead for all of them and warp 3 copies
+// scales.  All waits are bounded.
 //
 // Method: as gemm_pair.cu; the pages' deployment section (jsqmd.com) asks for
 // quantised experts.
@@ -60,28 +61,36 @@ constexpr uint32_t kATile = 128 * kRowBytes;
 constexpr int kChunkK = 512;             // values of K per scale chunk (16 scale bytes)
 constexpr int kScSlots = 4;              // scale chunks in shared memory
 constexpr uint32_t kScA = 128 * 16;      // bytes of a chunk's weight scales
+constexpr int kHalfK = 256;              // values of K per scale buffer in tensor memory
+constexpr int kWorkSlots = 4;            // units announced ahead by the scheduling warp
+constexpr int kWorkInts = 12;
 constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kAccCols = kMaxN;     // accumulators at columns 0 and 192
-constexpr uint32_t kScCol = 2 * kAccCols;  // scale buffers at columns 384 and 448
-constexpr uint32_t kScBuf = 64;          // four words of K: 4 columns of A, 4 unused, 8 of B each
 constexpr int kColChunk = 16;            // accumulator columns per epilogue step
 constexpr uint32_t kXchg = 4 * 2 * 2 * 8 * 32 * 4;  // [warp pair][buf][a|b][8][32] fp32
 constexpr int kMaxPairs = 80;            // pairs a launch may use (74 on 148 SMs)
 constexpr int kParts = 2 * kMaxPairs;    // partial units: two per pair
 constexpr size_t kCounters = static_cast<size_t>(kMaxPairs) * 2 * kEpiWarps;
 
-// Shared memory by the largest token tile: fewer token rows leave room for
-// more stages, which a weight stream needs in flight.
+// Layout by the largest token tile: fewer token rows leave room for more
+// stages, which a weight stream needs in flight.
 template <int NMAX>
-struct Smem {
+struct Shape {
     static constexpr uint32_t kBTile = NMAX / 2 * kRowBytes;
     static constexpr uint32_t kStage = kATile + kBTile;
     static constexpr int kStages = NMAX == 192 ? 6 : NMAX == 96 ? 7 : 9;
     static constexpr uint32_t kScSlot = kScA + NMAX * 16;
-    static constexpr int kBarriers = 2 * kStages + 2 * kScSlots + 2 * 2 + 2 * 2 + 1 + 8;
+    // Tensor memory: two accumulators of NMAX columns, then kScBufs buffers
+    // of the scales of 256 values of K.  128 values are one 32-bit word a
+    // row: 4 columns of A's scales, then NMAX / 32 of B's.
+    static constexpr uint32_t kWord = NMAX == 192 ? 12 : 8;
+    static constexpr uint32_t kScCol = 2 * NMAX;
+    static constexpr int kScBufs = NMAX == 192 ? 5 : 8;
+    static_assert(kScCol + kScBufs * 2 * kWord <= kTmemCols, "tensor memory");
+    static constexpr int kBarriers = 2 * kStages + 2 * kScSlots + 2 * 2 + 2 * kScBufs +
+                                     2 * kWorkSlots + 1 + 8;
     static constexpr size_t kBytes = 1024 /* alignment slack */ + kStages * kStage +
                                      kScSlots * kScSlot + kXchg + kBarriers * 8 + 64 +
-                                     2 * (kMaxE + 1) * sizeof(int32_t);
+                                     kWorkSlots * kWorkInts * 4 + 2 * (kMaxE + 1) * sizeof(int32_t);
     static_assert(kBytes <= 227 * 1024, "shared memory");
     static_assert(kBTile % 1024 == 0, "swizzle atom");
 };
@@ -149,15 +158,50 @@ struct Work {
     int part, first, last, cut;
 };
 
-// The sequence of work of one pair; every role of both CTAs walks it alike.
+// The scheduling warp's announcement of a unit, read by every other role.
+__device__ __forceinline__ void put(volatile int32_t *s, const Work &w)
+{
+    s[0] = w.e;
+    s[1] = w.blk;
+    s[2] = w.r0;
+    s[3] = w.valid;
+    s[4] = w.n;
+    s[5] = w.c0;
+    s[6] = w.c1;
+    s[7] = w.part;
+    s[8] = w.first;
+    s[9] = w.last;
+    s[10] = w.cut;
+}
+
+__device__ __forceinline__ void get(const int32_t *s, Work &w)
+{
+    const int4 a = reinterpret_cast<const int4 *>(s)[0];
+    const int4 b = reinterpret_cast<const int4 *>(s)[1];
+    const int4 c = reinterpret_cast<const int4 *>(s)[2];
+    w.e = a.x;
+    w.blk = a.y;
+    w.r0 = a.z;
+    w.valid = a.w;
+    w.n = b.x;
+    w.c0 = b.y;
+    w.c1 = b.z;
+    w.part = b.w;
+    w.first = c.x;
+    w.last = c.y;
+    w.cut = c.z;
+}
+
+// The sequence of work of one pair; both CTAs walk it alike.
 struct Walk {
     int pair, pairs, units, whole, chunks;   // units [whole, units) may be cut
+    int cutters;                             // pairs that share those: no range is empty
     int u;                                   // next whole unit
     long long it, end, items;                // chunk items of the cut units
     int first_cut;                           // the first cut unit of this pair
 
-    // Units whole, whole + 1, .. share `items` chunks of K; pair p has
-    // [items p / pairs, items (p + 1) / pairs) of them.
+    // Units whole, whole + 1, .. hold `items` chunks of K; pair p < cutters
+    // has [items p / cutters, items (p + 1) / cutters) of them.
     __device__ __forceinline__ void start(int pair_, int pairs_, int units_, int whole_, int chunks_)
     {
         pair = pair_;
@@ -167,14 +211,18 @@ struct Walk {
         chunks = chunks_;
         u = pair;
         items = static_cast<long long>(units - whole) * chunks;
-        it = items * pair / pairs;
-        end = items * (pair + 1) / pairs;
+        cutters = items < pairs ? static_cast<int>(items) : pairs;
+        it = end = 0;
+        if (pair < cutters) {
+            it = items * pair / cutters;
+            end = items * (pair + 1) / cutters;
+        }
         first_cut = static_cast<int>(it / chunks);
     }
 
     __device__ __forceinline__ int owner(long long item) const
     {
-        return static_cast<int>(((item + 1) * pairs - 1) / items);
+        return static_cast<int>(((item + 1) * cutters - 1) / items);
     }
 
     // Next unit and its chunks; false when the pair is done.
@@ -209,7 +257,7 @@ struct Walk {
     // The slot in which pair p stores its part of cut unit c.
     __device__ __forceinline__ int part_of(int p, int c) const
     {
-        return 2 * p + (static_cast<int>((items * p / pairs) / chunks) == c ? 0 : 1);
+        return 2 * p + (static_cast<int>((items * p / cutters) / chunks) == c ? 0 : 1);
     }
 };
 
@@ -358,10 +406,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                    const __grid_constant__ CUtensorMap tmS3, const __grid_constant__ CUtensorMap tmXs,
                    const GemmParams p)
 {
-    using SM = Smem<NMAX>;
+    using SM = Shape<NMAX>;
     constexpr int kStages = SM::kStages;
     constexpr int kStageK = FMT == kMxE4M3 ? 128 : 256;      // values of K per stage
     constexpr int kStagesPerChunk = kChunkK / kStageK;
+    constexpr int kStagesPerHalf = kHalfK / kStageK;
     // Bytes a CTA's copies count per stage: a spread copy counts the 4-bit
     // codes it moves, not the shared memory it covers.
     constexpr uint32_t kStageTx = SM::kBTile + (FMT == kMxE4M3 ? kATile / 2 : kATile);
@@ -381,19 +430,23 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *cempty = cfull + kScSlots;    // [kScSlots]
     uint64_t *tfull = cempty + kScSlots;    // [2] accumulator
     uint64_t *tempty = tfull + 2;           // [2]
-    uint64_t *sfull = tempty + 2;           // [2] scale chunk in tensor memory
-    uint64_t *sempty = sfull + 2;           // [2]
-    uint64_t *drain = sempty + 2;           // [1]
+    uint64_t *sfull = tempty + 2;           // [kScBufs] scales in tensor memory
+    uint64_t *sempty = sfull + SM::kScBufs; // [kScBufs]
+    uint64_t *wfull = sempty + SM::kScBufs; // [kWorkSlots] unit announced
+    uint64_t *wempty = wfull + kWorkSlots;  // [kWorkSlots]
+    uint64_t *drain = wempty + kWorkSlots;  // [1]
     uint64_t *xbar = drain + 1;             // [4 warp pairs][2 exchange buffers]
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(xbar + 8);
+    int32_t *s_work = reinterpret_cast<int32_t *>((reinterpret_cast<uintptr_t>(xbar + 8) + 15) & ~static_cast<uintptr_t>(15));
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(s_work + kWorkSlots * kWorkInts);
     volatile uint32_t *abort_flag = tmem_slot + 1;
-    int32_t *s_off = reinterpret_cast<int32_t *>(tmem_slot + 16);
+    int32_t *s_off = reinterpret_cast<int32_t *>(tmem_slot + 8);
     int32_t *s_pre = s_off + (kMaxE + 1);
 
     const int E = p.offsets ? p.E : 1;
     const int blocks = (p.N + p.rows_blk - 1) / p.rows_blk;
     const int chunks = (p.K + kChunkK - 1) / kChunkK;
     const int ksteps = (p.K + kStageK - 1) / kStageK;
+    const int halves = (p.K + kHalfK - 1) / kHalfK;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -407,8 +460,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int b = 0; b < 2; ++b) {
             ptx::mbar_init(&tfull[b], 1);
             ptx::mbar_init(&tempty[b], 2 * kEpiWarps);
+        }
+        for (int b = 0; b < SM::kScBufs; ++b) {
             ptx::mbar_init(&sfull[b], 8);
             ptx::mbar_init(&sempty[b], 1);
+        }
+        for (int b = 0; b < kWorkSlots; ++b) {
+            ptx::mbar_init(&wfull[b], 1);
+            // two copying warps, scales, epilogue; the even CTA's MMAs
+            ptx::mbar_init(&wempty[b], 2 + 4 + kEpiWarps + (leader ? 1 : 0));
         }
         ptx::mbar_init(drain, 1);
         for (int b = 0; b < 8; ++b) ptx::mbar_init(&xbar[b], 64);
@@ -475,68 +535,79 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int units = s_pre[E];
     const int pairs = static_cast<int>(gridDim.x >> 1);
     const int whole = plan(units, pairs, chunks);
-    Walk walk;
-    walk.start(static_cast<int>(blockIdx.x >> 1), pairs, units, whole, chunks);
 
     // Shared::cluster addresses of the even CTA's barriers.
     const uint32_t full0 = ptx::mapa_shared(ptx::smem_addr(full), 0);
     const uint32_t tempty0 = ptx::mapa_shared(ptx::smem_addr(tempty), 0);
     const uint32_t sfull0 = ptx::mapa_shared(ptx::smem_addr(sfull), 0);
 
+    // Takes the next announced unit; false at the end (or after a failure).
+    // `who` reads the slot and arrives once.
+    uint32_t wslot = 0, wphase = 0;
     Work w;
-    int unit;
-    if (warp == 0) {
+    auto next_unit = [&](bool warp_wide) -> bool {
+        const bool ok = warp_wide ? wait_cl_warp(&wfull[wslot], wphase, abort_flag, p.err, kErrTimeoutEpi)
+                                  : wait_cl(&wfull[wslot], wphase, abort_flag, p.err, kErrTimeoutEpi);
+        if (!ok) return false;
+        get(s_work + wslot * kWorkInts, w);
+        if (warp_wide) __syncwarp();
+        if (!warp_wide || lane == 0) ptx::mbar_arrive(&wempty[wslot]);
+        if (++wslot == kWorkSlots) {
+            wslot = 0;
+            wphase ^= 1u;
+        }
+        return w.e >= 0;
+    };
+    if (warp == 2) {
+        // Scheduling: decodes the pair's units ahead of the other roles.
+        if (lane == 0) {
+            Walk walk;
+            walk.start(static_cast<int>(blockIdx.x >> 1), pairs, units, whole, chunks);
+            bool more = true;
+            while (more) {
+                int unit = 0;
+                more = walk.next(w, unit);
+                if (more) place<NMAX>(w, unit, s_off, s_pre, E);
+                else w.e = -1;
+                if (!wait_cl(&wempty[wslot], wphase ^ 1u, abort_flag, p.err, kErrTimeoutEpi)) break;
+                put(s_work + wslot * kWorkInts, w);
+                ptx::mbar_arrive(&wfull[wslot]);
+                if (++wslot == kWorkSlots) {
+                    wslot = 0;
+                    wphase ^= 1u;
+                }
+            }
+        }
+    } else if (warp == 0) {
         if (lane == 0) {
             uint32_t stage = 0, phase = 0, issued = 0;
-            uint32_t slot = 0, cphase = 0, cissued = 0;
-            uint32_t last_parity[kStages], clast[kScSlots];
+            uint32_t last_parity[kStages];
 #pragma unroll
             for (int s = 0; s < kStages; ++s) last_parity[s] = 0;
-#pragma unroll
-            for (int s = 0; s < kScSlots; ++s) clast[s] = 0;
             const uint64_t pol = ptx::policy_evict_normal();
             bool stop = false;
-            while (!stop && walk.next(w, unit)) {
-                place<NMAX>(w, unit, s_off, s_pre, E);
+            while (!stop && next_unit(false)) {
                 const int arow = w.e * p.N + w.blk * p.rows_blk + static_cast<int>(cta) * (p.rows_blk / 2);
                 const int brow = w.r0 + static_cast<int>(cta) * (w.n >> 1);
-                for (int c = w.c0; c < w.c1 && !stop; ++c) {
-                    if (!wait_cl(&cempty[slot], cphase ^ 1u, abort_flag, p.err, kErrTimeoutTma)) {
+                const int k1 = min(w.c1 * kStagesPerChunk, ksteps);
+                for (int ks = w.c0 * kStagesPerChunk; ks < k1; ++ks) {
+                    if (!wait_cl(&empty[stage], phase ^ 1u, abort_flag, p.err, kErrTimeoutMma)) {
                         stop = true;
                         break;
                     }
-                    uint8_t *sc = scales + slot * SM::kScSlot;
-                    ptx::mbar_arrive_expect_tx(&cfull[slot], SM::kScSlot);
-                    ptx::tma_load_2d(sc, &tmS1, &cfull[slot], c * 16, arow);
-                    if (GATED) ptx::tma_load_2d(sc + kScA / 2, &tmS3, &cfull[slot], c * 16, arow);
-                    ptx::tma_load_2d(sc + kScA, &tmXs, &cfull[slot], c * 16, w.r0);
-                    cissued |= 1u << slot;
-                    clast[slot] = cphase;
-                    if (++slot == kScSlots) {
-                        slot = 0;
-                        cphase ^= 1u;
-                    }
-                    for (int i = 0; i < kStagesPerChunk; ++i) {
-                        const int ks = c * kStagesPerChunk + i;
-                        if (ks >= ksteps) break;
-                        if (!wait_cl(&empty[stage], phase ^ 1u, abort_flag, p.err, kErrTimeoutMma)) {
-                            stop = true;
-                            break;
-                        }
-                        uint8_t *sa = smem + stage * SM::kStage;
-                        const uint32_t fb = full0 + 8 * stage;
-                        if (leader) ptx::mbar_arrive_expect_tx(&full[stage], 2 * kStageTx);
-                        // 128 bytes of a row in shared memory: the coordinate
-                        // counts codes (the spread copy) or bytes
-                        ptx::tma_load_2d_pair(sa, &tmW1, fb, ks * 128, arow, pol);
-                        if (GATED) ptx::tma_load_2d_pair(sa + kATile / 2, &tmW3, fb, ks * 128, arow, pol);
-                        ptx::tma_load_2d_pair(sa + kATile, &tmX, fb, ks * 128, brow, pol);
-                        issued |= 1u << stage;
-                        last_parity[stage] = phase;
-                        if (++stage == static_cast<uint32_t>(kStages)) {
-                            stage = 0;
-                            phase ^= 1u;
-                        }
+                    uint8_t *sa = smem + stage * SM::kStage;
+                    const uint32_t fb = full0 + 8 * stage;
+                    if (leader) ptx::mbar_arrive_expect_tx(&full[stage], 2 * kStageTx);
+                    // 128 bytes of a row in shared memory: the coordinate
+                    // counts codes (the spread copy) or bytes
+                    ptx::tma_load_2d_pair(sa, &tmW1, fb, ks * 128, arow, pol);
+                    if (GATED) ptx::tma_load_2d_pair(sa + kATile / 2, &tmW3, fb, ks * 128, arow, pol);
+                    ptx::tma_load_2d_pair(sa + kATile, &tmX, fb, ks * 128, brow, pol);
+                    issued |= 1u << stage;
+                    last_parity[stage] = phase;
+                    if (++stage == static_cast<uint32_t>(kStages)) {
+                        stage = 0;
+                        phase ^= 1u;
                     }
                 }
             }
@@ -546,59 +617,97 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (leader)
                 for (int s = 0; s < kStages; ++s)
                     if (issued & (1u << s)) drain_wait(&full[s], last_parity[s]);
-            for (int s = 0; s < kScSlots; ++s)
-                if (cissued & (1u << s)) drain_wait(&cfull[s], clast[s]);
         }
-    } else if (warp == 1) {
-        if (lane == 0 && leader) {
-            uint32_t stage = 0, phase = 0, sc = 0;
+    } else if (warp == 3) {
+        // Copies of scales: few bytes in many short rows, so they take longer
+        // than a stage's operands; their own ring runs up to kScSlots chunks
+        // ahead.
+        if (lane == 0) {
+            uint32_t slot = 0, cphase = 0, issued = 0;
+            uint32_t last_parity[kScSlots];
+#pragma unroll
+            for (int s = 0; s < kScSlots; ++s) last_parity[s] = 0;
             bool stop = false;
-            for (uint32_t i = 0; !stop && walk.next(w, unit); ++i) {
-                place<NMAX>(w, unit, s_off, s_pre, E);
-                const uint32_t buf = i & 1u;
-                if (!wait_cl(&tempty[buf], ((i >> 1) & 1u) ^ 1u, abort_flag, p.err, kErrTimeoutEpi))
-                    break;
-                ptx::tc_fence_after();
-                const uint32_t dacc = tmem + buf * kAccCols;
-                uint32_t acc = 0;
-                for (int c = w.c0; c < w.c1 && !stop; ++c, ++sc) {
-                    const uint32_t sb = sc & 1u;
-                    if (!wait_cl(&sfull[sb], (sc >> 1) & 1u, abort_flag, p.err, kErrTimeoutTma)) {
+            while (!stop && next_unit(false)) {
+                const int arow = w.e * p.N + w.blk * p.rows_blk + static_cast<int>(cta) * (p.rows_blk / 2);
+                for (int c = w.c0; c < w.c1; ++c) {
+                    if (!wait_cl(&cempty[slot], cphase ^ 1u, abort_flag, p.err, kErrTimeoutTma)) {
                         stop = true;
                         break;
                     }
-                    ptx::tc_fence_after();
-                    const uint32_t scol = tmem + kScCol + sb * kScBuf;
-                    for (int j = 0; j < kStagesPerChunk; ++j) {
-                        const int ks = c * kStagesPerChunk + j;
-                        if (ks >= ksteps) break;
+                    uint8_t *sc = scales + slot * SM::kScSlot;
+                    ptx::mbar_arrive_expect_tx(&cfull[slot], SM::kScSlot);
+                    ptx::tma_load_2d(sc, &tmS1, &cfull[slot], c * 16, arow);
+                    if (GATED) ptx::tma_load_2d(sc + kScA / 2, &tmS3, &cfull[slot], c * 16, arow);
+                    ptx::tma_load_2d(sc + kScA, &tmXs, &cfull[slot], c * 16, w.r0);
+                    issued |= 1u << slot;
+                    last_parity[slot] = cphase;
+                    if (++slot == kScSlots) {
+                        slot = 0;
+                        cphase ^= 1u;
+                    }
+                }
+            }
+            for (int s = 0; s < kScSlots; ++s)
+                if (issued & (1u << s)) drain_wait(&cfull[s], last_parity[s]);
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && leader) {
+            uint32_t stage = 0, phase = 0, sb = 0, sphase = 0;
+            // Descriptors differ in their start address (16-byte units) only.
+            const uint64_t desc0 = ptx::sw128_kmajor_desc(0);
+            const uint32_t smem16 = ptx::smem_addr(smem) >> 4;
+            const uint32_t fmt_a = FMT == kMxE4M3 ? ptx::kMxf8f6f4E2M1 : ptx::kMxf4E2M1;
+            const uint32_t fmt_b = FMT == kMxE4M3 ? ptx::kMxf8f6f4E4M3 : ptx::kMxf4E2M1;
+            const int last_half = p.K % kHalfK ? 2 : 4;   // MMAs of the last e2m1 stage
+            bool stop = false;
+            for (uint32_t i = 0; !stop && next_unit(false); ++i) {
+                const uint32_t buf = i & 1u;
+                uint32_t idesc[4];
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    idesc[kk] = ptx::idesc_mx(256, w.n, fmt_a, fmt_b, FMT == kMxE4M3 ? kk : 2 * (kk & 1));
+                if (!wait_cl(&tempty[buf], ((i >> 1) & 1u) ^ 1u, abort_flag, p.err, kErrTimeoutEpi))
+                    break;
+                ptx::tc_fence_after();
+                const uint32_t dacc = tmem + buf * NMAX;
+                uint32_t acc = 0;
+                const int h1 = min(2 * w.c1, halves);
+                for (int h = 2 * w.c0; h < h1; ++h) {
+                    if (!wait_cl(&sfull[sb], sphase, abort_flag, p.err, kErrTimeoutTma)) {
+                        stop = true;
+                        break;
+                    }
+                    const uint32_t word0 = tmem + SM::kScCol + sb * (2 * SM::kWord);
+#pragma unroll
+                    for (int j = 0; j < kStagesPerHalf; ++j) {
+                        if (h * kStagesPerHalf + j >= ksteps) break;
                         if (!wait_cl(&full[stage], phase, abort_flag, p.err, kErrTimeoutTma)) {
                             stop = true;
                             break;
                         }
                         ptx::tc_fence_after();
-                        const uint32_t sa = ptx::smem_addr(smem + stage * SM::kStage);
-                        const uint32_t sx = sa + kATile;
+                        const uint32_t a16 = smem16 + stage * (SM::kStage >> 4);
+                        const uint64_t da = desc0 | a16;
+                        const uint64_t db = desc0 | (a16 + (kATile >> 4));
+                        // e4m3 rows: 4 x 32 values, bytes 0..3 of one word;
+                        // e2m1 rows: 4 x 64 values, two bytes each of two
+                        // words, and only 2 x 64 at an odd end of K
+                        const int n_mma = FMT == kMxE4M3 || h + 1 < halves ? 4 : last_half;
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk) {
-                            const uint64_t da = ptx::sw128_kmajor_desc(sa + kk * 32);
-                            const uint64_t db = ptx::sw128_kmajor_desc(sx + kk * 32);
-                            if constexpr (FMT == kMxE4M3) {
-                                const uint32_t word = scol + 16 * j;  // 4 scales of 32: byte kk
-                                ptx::tc_mma_mxf8f6f4_pair(
-                                    dacc, da, db,
-                                    ptx::idesc_mx(256, w.n, ptx::kMxf8f6f4E2M1, ptx::kMxf8f6f4E4M3, kk),
-                                    word, word + 8, acc);
-                            } else {
-                                // a stage may end after its first 128 values
-                                if (kk >= 2 && ks * kStageK + 128 >= p.K) break;
-                                const uint32_t word = scol + 16 * (2 * j + (kk >> 1));
-                                ptx::tc_mma_mxf4_pair(
-                                    dacc, da, db,
-                                    ptx::idesc_mx(256, w.n, ptx::kMxf4E2M1, ptx::kMxf4E2M1, 2 * (kk & 1)),
-                                    word, word + 8, acc);
+                            if (kk < n_mma) {
+                                if constexpr (FMT == kMxE4M3) {
+                                    const uint32_t word = word0 + SM::kWord * j;
+                                    ptx::tc_mma_mxf8f6f4_pair(dacc, da + 2 * kk, db + 2 * kk, idesc[kk], word,
+                                                              word + 4, acc);
+                                } else {
+                                    const uint32_t word = word0 + SM::kWord * (kk >> 1);
+                                    ptx::tc_mma_mxf4_pair(dacc, da + 2 * kk, db + 2 * kk, idesc[kk], word,
+                                                          word + 4, acc);
+                                }
+                                acc = 1;
                             }
-                            acc = 1;
                         }
                         ptx::tc_commit_pair(&empty[stage], 0x3);
                         if (++stage == static_cast<uint32_t>(kStages)) {
@@ -606,7 +715,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                             phase ^= 1u;
                         }
                     }
-                    if (!stop) ptx::tc_commit_pair(&sempty[sb], 0x3);
+                    if (stop) break;
+                    ptx::tc_commit_pair(&sempty[sb], 0x3);
+                    if (++sb == static_cast<uint32_t>(SM::kScBufs)) {
+                        sb = 0;
+                        sphase ^= 1u;
+                    }
                 }
                 if (!stop) ptx::tc_commit_pair(&tfull[buf], 0x3);
             }
@@ -617,17 +731,16 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp >= 4 && warp < 8) {
         // Scales: shared memory (row-major, 16 bytes a row) to this warp's
         // lane quarter of tensor memory.
-        const uint32_t tq = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + kScCol;
-        uint32_t slot = 0, cphase = 0, sc = 0;
+        const uint32_t tq = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + SM::kScCol;
+        constexpr int kB = NMAX / 32;
+        uint32_t slot = 0, cphase = 0, sb = 0, sphase = 0;
         bool stop = false;
-        while (!stop && walk.next(w, unit)) {
-            place<NMAX>(w, unit, s_off, s_pre, E);
-            for (int c = w.c0; c < w.c1; ++c, ++sc) {
+        while (!stop && next_unit(true)) {
+            for (int c = w.c0; c < w.c1 && !stop; ++c) {
                 if (!wait_cl_warp(&cfull[slot], cphase, abort_flag, p.err, kErrTimeoutTma)) {
                     stop = true;
                     break;
                 }
-                constexpr int kB = NMAX / 32;
                 const uint4 *src = reinterpret_cast<const uint4 *>(scales + slot * SM::kScSlot);
                 uint4 a[4], b[kB];
 #pragma unroll
@@ -640,27 +753,37 @@ __global__ void __launch_bounds__(kThreads, 1)
                     slot = 0;
                     cphase ^= 1u;
                 }
-                const uint32_t sb = sc & 1u;
-                if (!wait_cl_warp(&sempty[sb], ((sc >> 1) & 1u) ^ 1u, abort_flag, p.err, kErrTimeoutMma)) {
-                    stop = true;
-                    break;
-                }
-                ptx::tc_fence_after();
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t r[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        r[i] = 0u;
-                        if (i < 4) r[i] = reinterpret_cast<const uint32_t *>(&a[i])[j];
-                        if (i >= 8 && i - 8 < kB) r[i] = reinterpret_cast<const uint32_t *>(&b[i - 8])[j];
+                for (int h = 0; h < 2; ++h) {
+                    if (2 * c + h >= halves) break;
+                    if (!wait_cl_warp(&sempty[sb], sphase ^ 1u, abort_flag, p.err, kErrTimeoutMma)) {
+                        stop = true;
+                        break;
                     }
-                    ptx::tmem_st16(tq + sb * kScBuf + 16 * j, r);
+                    ptx::tc_fence_after();
+                    uint32_t r[2 * SM::kWord];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j)
+#pragma unroll
+                        for (int i = 0; i < static_cast<int>(SM::kWord); ++i) {
+                            uint32_t v = 0u;
+                            if (i < 4) v = reinterpret_cast<const uint32_t *>(&a[i])[2 * h + j];
+                            else if (i - 4 < kB) v = reinterpret_cast<const uint32_t *>(&b[i - 4])[2 * h + j];
+                            r[SM::kWord * j + i] = v;
+                        }
+                    const uint32_t dst = tq + sb * (2 * SM::kWord);
+                    ptx::tmem_st16(dst, *reinterpret_cast<const uint32_t(*)[16]>(&r[0]));
+                    if constexpr (SM::kWord == 12)
+                        ptx::tmem_st8(dst + 16, *reinterpret_cast<const uint32_t(*)[8]>(&r[16]));
+                    ptx::tc_wait_st();
+                    ptx::tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive_pair(sfull0 + 8 * sb);
+                    if (++sb == static_cast<uint32_t>(SM::kScBufs)) {
+                        sb = 0;
+                        sphase ^= 1u;
+                    }
                 }
-                ptx::tc_wait_st();
-                ptx::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive_cluster(sfull0 + 8 * sb);
             }
         }
     } else if (warp >= 8) {
@@ -671,16 +794,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
         const int wpair = (q & 1) + 2 * half;  // (a, b) warp pairs: quarters (0,2) and (1,3)
         const bool is_a = q < 2;               // lanes 0..63: W1 products (gated)
+        Walk walk;  // for the slots of other pairs' parts
+        walk.start(static_cast<int>(blockIdx.x >> 1), pairs, units, whole, chunks);
         float *xa = xchg + wpair * (2 * 2 * 8 * 32);
         uint32_t xuse[2] = {0u, 0u};
         int xb = 0;
         bool stop = false;
-        for (uint32_t i = 0; !stop && walk.next(w, unit); ++i) {
-            place<NMAX>(w, unit, s_off, s_pre, E);
+        for (uint32_t i = 0; !stop && next_unit(true); ++i) {
             const uint32_t buf = i & 1u;
             if (!wait_cl_warp(&tfull[buf], (i >> 1) & 1u, abort_flag, p.err, kErrTimeoutMma)) break;
             ptx::tc_fence_after();
-            const uint32_t tb = tmem + lane_base + buf * kAccCols;
+            const uint32_t tb = tmem + lane_base + buf * NMAX;
             const int nch = w.n / kColChunk;
             // output column of this lane: product, or h of the lane's quarter
             const int o = GATED ? w.blk * 128 + static_cast<int>(cta) * 64 + (q & 1) * 32 + lane
@@ -743,7 +867,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
             if (lane == 0) {
                 if (leader) ptx::mbar_arrive(&tempty[buf]);
-                else ptx::mbar_arrive_cluster(tempty0 + 8 * buf);
+                else ptx::mbar_arrive_pair(tempty0 + 8 * buf);
             }
             if (w.part >= 0) {
                 // The last warp to arrive (of the warp's own columns and
@@ -830,7 +954,7 @@ int part_cols(int S) { return std::min(kMaxN, (S + 15) / 16 * 16); }
 template <int FMT, bool GATED, int NMAX>
 cudaError_t launch_t(const MxGemmLaunch &a, cudaStream_t s)
 {
-    using SM = Smem<NMAX>;
+    using SM = Shape<NMAX>;
     const uint64_t wrows = static_cast<uint64_t>(a.E) * a.N;
     const uint32_t abox = GATED ? 64 : 128;
     const int xbytes = FMT == kMxE4M3 ? a.K : a.K / 2;

@@ -163,6 +163,7 @@ SIZES = [
     ([1], 128, 8), ([3], 256, 136), ([2, 0, 1], 128, 1000), ([0, 5, 0, 0], 384, 264),
     ([37, 0, 128, 1, 200, 64], 640, 392), ([191, 193, 192], 512, 520), ([700, 16], 1408, 264),
     ([1] * 40, 256, 256), ([2, 1], 14336, 512), ([17] * 9, 2048, 640),
+    ([1], 4096, 256), ([0, 3], 3584, 8), ([1] * 75, 3200, 256),   # cut units of fewer chunks than there are CTA pairs
 ]
 
 
@@ -239,7 +240,8 @@ def gated_ref(x, W1, W3, sizes, act):
 @pytest.mark.parametrize("fmt", [mx.E4M3, mx.E2M1])
 @pytest.mark.parametrize("act", [0, 1])
 @pytest.mark.parametrize("sizes,d,f", [([1], 128, 128), ([2, 0, 1], 256, 384), ([37, 0, 128, 1, 200, 64], 640, 256),
-                                       ([97, 95, 96], 512, 512), ([1] * 40, 256, 128), ([2, 1], 4096, 1408)])
+                                       ([97, 95, 96], 512, 512), ([1] * 40, 256, 128), ([2, 1], 4096, 1408),
+                                       ([1], 4096, 128), ([1] * 76, 2816, 128)])
 def test_gated_matches_formula(fmt, act, sizes, d, f):
     rng = np.random.default_rng(len(sizes) + d + f)
     E, R = len(sizes), sum(sizes)
