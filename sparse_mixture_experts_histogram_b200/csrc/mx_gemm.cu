@@ -63,7 +63,7 @@ constexpr int kScSlots = 4;              // scale chunks in shared memory
 constexpr uint32_t kScA = 128 * 16;      // bytes of a chunk's weight scales
 constexpr int kHalfK = 256;              // values of K per scale buffer in tensor memory
 constexpr int kWorkSlots = 4;            // units announced ahead by the scheduling warp
-constexpr int kWorkInts = 12;
+constexpr int kWorkInts = 16;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kColChunk = 16;            // accumulator columns per epilogue step
 constexpr uint32_t kXchg = 4 * 2 * 2 * 8 * 32 * 4;  // [warp pair][buf][a|b][8][32] fp32
@@ -176,20 +176,18 @@ __device__ __forceinline__ void put(volatile int32_t *s, const Work &w)
 
 __device__ __forceinline__ void get(const int32_t *s, Work &w)
 {
-    const int4 a = reinterpret_cast<const int4 *>(s)[0];
-    const int4 b = reinterpret_cast<const int4 *>(s)[1];
-    const int4 c = reinterpret_cast<const int4 *>(s)[2];
-    w.e = a.x;
-    w.blk = a.y;
-    w.r0 = a.z;
-    w.valid = a.w;
-    w.n = b.x;
-    w.c0 = b.y;
-    w.c1 = b.z;
-    w.part = b.w;
-    w.first = c.x;
-    w.last = c.y;
-    w.cut = c.z;
+    const int v = s[threadIdx.x & 15];
+    w.e = __shfl_sync(0xffffffffu, v, 0);
+    w.blk = __shfl_sync(0xffffffffu, v, 1);
+    w.r0 = __shfl_sync(0xffffffffu, v, 2);
+    w.valid = __shfl_sync(0xffffffffu, v, 3);
+    w.n = __shfl_sync(0xffffffffu, v, 4);
+    w.c0 = __shfl_sync(0xffffffffu, v, 5);
+    w.c1 = __shfl_sync(0xffffffffu, v, 6);
+    w.part = __shfl_sync(0xffffffffu, v, 7);
+    w.first = __shfl_sync(0xffffffffu, v, 8);
+    w.last = __shfl_sync(0xffffffffu, v, 9);
+    w.cut = __shfl_sync(0xffffffffu, v, 10);
 }
 
 // The sequence of work of one pair; both CTAs walk it alike.
@@ -417,9 +415,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
-    const int warp = threadIdx.x >> 5;
+    // Broadcast, so that the compiler knows them to be the same over a warp:
+    // the warps that issue copies and MMAs then keep addresses, descriptors
+    // and loop counters in uniform registers, which those instructions read.
+    // With one thread's own values every operand was moved over before each
+    // MMA: 150 cycles an MMA instead of 90.
+    const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
     const int lane = threadIdx.x & 31;
-    const uint32_t cta = ptx::cluster_ctarank();  // 0: issues the MMAs
+    const uint32_t cta = __shfl_sync(0xffffffffu, ptx::cluster_ctarank(), 0);  // 0: issues the MMAs
     const bool leader = (cta == 0);
 
     uint8_t *scales = smem + kStages * SM::kStage;
@@ -531,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Both CTAs' barriers are initialised before either CTA signals the other.
     ptx::cluster_sync();
     ptx::tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const int units = s_pre[E];
     const int pairs = static_cast<int>(gridDim.x >> 1);
     const int whole = plan(units, pairs, chunks);
@@ -542,16 +545,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t sfull0 = ptx::mapa_shared(ptx::smem_addr(sfull), 0);
 
     // Takes the next announced unit; false at the end (or after a failure).
-    // `who` reads the slot and arrives once.
     uint32_t wslot = 0, wphase = 0;
     Work w;
-    auto next_unit = [&](bool warp_wide) -> bool {
-        const bool ok = warp_wide ? wait_cl_warp(&wfull[wslot], wphase, abort_flag, p.err, kErrTimeoutEpi)
-                                  : wait_cl(&wfull[wslot], wphase, abort_flag, p.err, kErrTimeoutEpi);
-        if (!ok) return false;
+    auto next_unit = [&]() -> bool {
+        if (!wait_cl_warp(&wfull[wslot], wphase, abort_flag, p.err, kErrTimeoutEpi)) return false;
         get(s_work + wslot * kWorkInts, w);
-        if (warp_wide) __syncwarp();
-        if (!warp_wide || lane == 0) ptx::mbar_arrive(&wempty[wslot]);
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&wempty[wslot]);
         if (++wslot == kWorkSlots) {
             wslot = 0;
             wphase ^= 1u;
@@ -579,102 +579,97 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
         }
     } else if (warp == 0) {
-        if (lane == 0) {
-            uint32_t stage = 0, phase = 0, issued = 0;
-            uint32_t last_parity[kStages];
-#pragma unroll
-            for (int s = 0; s < kStages; ++s) last_parity[s] = 0;
-            const uint64_t pol = ptx::policy_evict_normal();
-            bool stop = false;
-            while (!stop && next_unit(false)) {
-                const int arow = w.e * p.N + w.blk * p.rows_blk + static_cast<int>(cta) * (p.rows_blk / 2);
-                const int brow = w.r0 + static_cast<int>(cta) * (w.n >> 1);
-                const int k1 = min(w.c1 * kStagesPerChunk, ksteps);
-                for (int ks = w.c0 * kStagesPerChunk; ks < k1; ++ks) {
-                    if (!wait_cl(&empty[stage], phase ^ 1u, abort_flag, p.err, kErrTimeoutMma)) {
-                        stop = true;
-                        break;
-                    }
-                    uint8_t *sa = smem + stage * SM::kStage;
-                    const uint32_t fb = full0 + 8 * stage;
+        const bool one = ptx::elect_one();
+        uint32_t stage = 0, phase = 0, issued = 0, last_parity = 0;  // bits by stage
+        const uint64_t pol = ptx::policy_evict_normal();
+        bool stop = false;
+        while (!stop && next_unit()) {
+            const int arow = w.e * p.N + w.blk * p.rows_blk + static_cast<int>(cta) * (p.rows_blk / 2);
+            const int brow = w.r0 + static_cast<int>(cta) * (w.n >> 1);
+            const int k1 = min(w.c1 * kStagesPerChunk, ksteps);
+            for (int ks = w.c0 * kStagesPerChunk; ks < k1; ++ks) {
+                if (!wait_cl_warp(&empty[stage], phase ^ 1u, abort_flag, p.err, kErrTimeoutMma)) {
+                    stop = true;
+                    break;
+                }
+                uint8_t *sa = smem + stage * SM::kStage;
+                const uint32_t fb = full0 + 8 * stage;
+                if (one) {
                     if (leader) ptx::mbar_arrive_expect_tx(&full[stage], 2 * kStageTx);
                     // 128 bytes of a row in shared memory: the coordinate
                     // counts codes (the spread copy) or bytes
                     ptx::tma_load_2d_pair(sa, &tmW1, fb, ks * 128, arow, pol);
                     if (GATED) ptx::tma_load_2d_pair(sa + kATile / 2, &tmW3, fb, ks * 128, arow, pol);
                     ptx::tma_load_2d_pair(sa + kATile, &tmX, fb, ks * 128, brow, pol);
-                    issued |= 1u << stage;
-                    last_parity[stage] = phase;
-                    if (++stage == static_cast<uint32_t>(kStages)) {
-                        stage = 0;
-                        phase ^= 1u;
-                    }
+                }
+                issued |= 1u << stage;
+                last_parity = (last_parity & ~(1u << stage)) | phase << stage;
+                if (++stage == static_cast<uint32_t>(kStages)) {
+                    stage = 0;
+                    phase ^= 1u;
                 }
             }
-            // No copy may still be landing in shared memory at exit.  The odd
-            // CTA's operand copies count on the even CTA's barriers, and the
-            // final cluster barrier orders its exit after this.
-            if (leader)
-                for (int s = 0; s < kStages; ++s)
-                    if (issued & (1u << s)) drain_wait(&full[s], last_parity[s]);
         }
+        // No copy may still be landing in shared memory at exit.  The odd
+        // CTA's operand copies count on the even CTA's barriers, and the
+        // final cluster barrier orders its exit after this.
+        if (leader && one)
+            for (int s = 0; s < kStages; ++s)
+                if (issued & (1u << s)) drain_wait(&full[s], last_parity >> s & 1u);
     } else if (warp == 3) {
         // Copies of scales: few bytes in many short rows, so they take longer
         // than a stage's operands; their own ring runs up to kScSlots chunks
         // ahead.
-        if (lane == 0) {
-            uint32_t slot = 0, cphase = 0, issued = 0;
-            uint32_t last_parity[kScSlots];
-#pragma unroll
-            for (int s = 0; s < kScSlots; ++s) last_parity[s] = 0;
-            bool stop = false;
-            while (!stop && next_unit(false)) {
-                const int arow = w.e * p.N + w.blk * p.rows_blk + static_cast<int>(cta) * (p.rows_blk / 2);
-                for (int c = w.c0; c < w.c1; ++c) {
-                    if (!wait_cl(&cempty[slot], cphase ^ 1u, abort_flag, p.err, kErrTimeoutTma)) {
-                        stop = true;
-                        break;
-                    }
-                    uint8_t *sc = scales + slot * SM::kScSlot;
+        const bool one = ptx::elect_one();
+        uint32_t slot = 0, cphase = 0, issued = 0, last_parity = 0;
+        bool stop = false;
+        while (!stop && next_unit()) {
+            const int arow = w.e * p.N + w.blk * p.rows_blk + static_cast<int>(cta) * (p.rows_blk / 2);
+            for (int c = w.c0; c < w.c1; ++c) {
+                if (!wait_cl_warp(&cempty[slot], cphase ^ 1u, abort_flag, p.err, kErrTimeoutTma)) {
+                    stop = true;
+                    break;
+                }
+                uint8_t *sc = scales + slot * SM::kScSlot;
+                if (one) {
                     ptx::mbar_arrive_expect_tx(&cfull[slot], SM::kScSlot);
                     ptx::tma_load_2d(sc, &tmS1, &cfull[slot], c * 16, arow);
                     if (GATED) ptx::tma_load_2d(sc + kScA / 2, &tmS3, &cfull[slot], c * 16, arow);
                     ptx::tma_load_2d(sc + kScA, &tmXs, &cfull[slot], c * 16, w.r0);
-                    issued |= 1u << slot;
-                    last_parity[slot] = cphase;
-                    if (++slot == kScSlots) {
-                        slot = 0;
-                        cphase ^= 1u;
-                    }
+                }
+                issued |= 1u << slot;
+                last_parity = (last_parity & ~(1u << slot)) | cphase << slot;
+                if (++slot == kScSlots) {
+                    slot = 0;
+                    cphase ^= 1u;
                 }
             }
-            for (int s = 0; s < kScSlots; ++s)
-                if (issued & (1u << s)) drain_wait(&cfull[s], last_parity[s]);
         }
+        if (one)
+            for (int s = 0; s < kScSlots; ++s)
+                if (issued & (1u << s)) drain_wait(&cfull[s], last_parity >> s & 1u);
     } else if (warp == 1) {
-        if (lane == 0 && leader) {
+        if (leader) {
+            const bool one = ptx::elect_one();
             uint32_t stage = 0, phase = 0, sb = 0, sphase = 0;
             // Descriptors differ in their start address (16-byte units) only.
             const uint64_t desc0 = ptx::sw128_kmajor_desc(0);
             const uint32_t smem16 = ptx::smem_addr(smem) >> 4;
             const uint32_t fmt_a = FMT == kMxE4M3 ? ptx::kMxf8f6f4E2M1 : ptx::kMxf4E2M1;
             const uint32_t fmt_b = FMT == kMxE4M3 ? ptx::kMxf8f6f4E4M3 : ptx::kMxf4E2M1;
-            const int last_half = p.K % kHalfK ? 2 : 4;   // MMAs of the last e2m1 stage
+            const bool odd_end = p.K % kHalfK != 0;   // the last e2m1 stage holds 128 values of K
             bool stop = false;
-            for (uint32_t i = 0; !stop && next_unit(false); ++i) {
+            for (uint32_t i = 0; !stop && next_unit(); ++i) {
                 const uint32_t buf = i & 1u;
-                uint32_t idesc[4];
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    idesc[kk] = ptx::idesc_mx(256, w.n, fmt_a, fmt_b, FMT == kMxE4M3 ? kk : 2 * (kk & 1));
-                if (!wait_cl(&tempty[buf], ((i >> 1) & 1u) ^ 1u, abort_flag, p.err, kErrTimeoutEpi))
+                const uint32_t idesc = ptx::idesc_mx(256, w.n, fmt_a, fmt_b, 0);
+                if (!wait_cl_warp(&tempty[buf], ((i >> 1) & 1u) ^ 1u, abort_flag, p.err, kErrTimeoutEpi))
                     break;
                 ptx::tc_fence_after();
                 const uint32_t dacc = tmem + buf * NMAX;
                 uint32_t acc = 0;
                 const int h1 = min(2 * w.c1, halves);
-                for (int h = 2 * w.c0; h < h1; ++h) {
-                    if (!wait_cl(&sfull[sb], sphase, abort_flag, p.err, kErrTimeoutTma)) {
+                for (int h = 2 * w.c0; h < h1 && !stop; ++h) {
+                    if (!wait_cl_warp(&sfull[sb], sphase, abort_flag, p.err, kErrTimeoutTma)) {
                         stop = true;
                         break;
                     }
@@ -682,7 +677,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < kStagesPerHalf; ++j) {
                         if (h * kStagesPerHalf + j >= ksteps) break;
-                        if (!wait_cl(&full[stage], phase, abort_flag, p.err, kErrTimeoutTma)) {
+                        if (!wait_cl_warp(&full[stage], phase, abort_flag, p.err, kErrTimeoutTma)) {
                             stop = true;
                             break;
                         }
@@ -690,43 +685,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const uint32_t a16 = smem16 + stage * (SM::kStage >> 4);
                         const uint64_t da = desc0 | a16;
                         const uint64_t db = desc0 | (a16 + (kATile >> 4));
-                        // e4m3 rows: 4 x 32 values, bytes 0..3 of one word;
-                        // e2m1 rows: 4 x 64 values, two bytes each of two
-                        // words, and only 2 x 64 at an odd end of K
-                        const int n_mma = FMT == kMxE4M3 || h + 1 < halves ? 4 : last_half;
+                        if (one) {
+                            if constexpr (FMT == kMxE4M3) {
+                                // 4 x 32 values, bytes 0..3 of one word
+                                const uint32_t word = word0 + SM::kWord * j;
 #pragma unroll
-                        for (int kk = 0; kk < 4; ++kk) {
-                            if (kk < n_mma) {
-                                if constexpr (FMT == kMxE4M3) {
-                                    const uint32_t word = word0 + SM::kWord * j;
-                                    ptx::tc_mma_mxf8f6f4_pair(dacc, da + 2 * kk, db + 2 * kk, idesc[kk], word,
-                                                              word + 4, acc);
-                                } else {
-                                    const uint32_t word = word0 + SM::kWord * (kk >> 1);
-                                    ptx::tc_mma_mxf4_pair(dacc, da + 2 * kk, db + 2 * kk, idesc[kk], word,
-                                                          word + 4, acc);
+                                for (int kk = 0; kk < 4; ++kk)
+                                    ptx::tc_mma_mxf8f6f4_pair(dacc, da + 2 * kk, db + 2 * kk,
+                                                              idesc + ptx::idesc_mx_sf(kk), word, word + 4,
+                                                              kk ? 1u : acc);
+                            } else {
+                                // 4 x 64 values, two bytes each of two words
+#pragma unroll
+                                for (int kk = 0; kk < 2; ++kk)
+                                    ptx::tc_mma_mxf4_pair(dacc, da + 2 * kk, db + 2 * kk,
+                                                          idesc + ptx::idesc_mx_sf(2 * kk), word0, word0 + 4,
+                                                          kk ? 1u : acc);
+                                if (!odd_end || h + 1 < halves) {
+#pragma unroll
+                                    for (int kk = 2; kk < 4; ++kk)
+                                        ptx::tc_mma_mxf4_pair(dacc, da + 2 * kk, db + 2 * kk,
+                                                              idesc + ptx::idesc_mx_sf(2 * (kk - 2)),
+                                                              word0 + SM::kWord, word0 + SM::kWord + 4, 1u);
                                 }
-                                acc = 1;
                             }
+                            ptx::tc_commit_pair(&empty[stage], 0x3);
                         }
-                        ptx::tc_commit_pair(&empty[stage], 0x3);
+                        acc = 1;
                         if (++stage == static_cast<uint32_t>(kStages)) {
                             stage = 0;
                             phase ^= 1u;
                         }
                     }
                     if (stop) break;
-                    ptx::tc_commit_pair(&sempty[sb], 0x3);
+                    if (one) ptx::tc_commit_pair(&sempty[sb], 0x3);
                     if (++sb == static_cast<uint32_t>(SM::kScBufs)) {
                         sb = 0;
                         sphase ^= 1u;
                     }
                 }
-                if (!stop) ptx::tc_commit_pair(&tfull[buf], 0x3);
+                if (!stop && one) ptx::tc_commit_pair(&tfull[buf], 0x3);
             }
             // Every MMA issued above has finished once this arrives.
-            ptx::tc_commit_pair(drain, 0x1);
-            drain_wait(drain, 0u);
+            if (one) {
+                ptx::tc_commit_pair(drain, 0x1);
+                drain_wait(drain, 0u);
+            }
         }
     } else if (warp >= 4 && warp < 8) {
         // Scales: shared memory (row-major, 16 bytes a row) to this warp's
@@ -735,7 +739,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int kB = NMAX / 32;
         uint32_t slot = 0, cphase = 0, sb = 0, sphase = 0;
         bool stop = false;
-        while (!stop && next_unit(true)) {
+        while (!stop && next_unit()) {
             for (int c = w.c0; c < w.c1 && !stop; ++c) {
                 if (!wait_cl_warp(&cfull[slot], cphase, abort_flag, p.err, kErrTimeoutTma)) {
                     stop = true;
@@ -800,7 +804,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t xuse[2] = {0u, 0u};
         int xb = 0;
         bool stop = false;
-        for (uint32_t i = 0; !stop && next_unit(true); ++i) {
+        for (uint32_t i = 0; !stop && next_unit(); ++i) {
             const uint32_t buf = i & 1u;
             if (!wait_cl_warp(&tfull[buf], (i >> 1) & 1u, abort_flag, p.err, kErrTimeoutMma)) break;
             ptx::tc_fence_after();

@@ -33,6 +33,17 @@ __device__ __forceinline__ void fence_barrier_init()
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
 }
 
+// True in one lane of a converged warp, always the same one.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "elect.sync _|p, 0xffffffff;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}\n"
+                 : "=r"(ok));
+    return ok != 0;
+}
+
 __device__ __forceinline__ void mbar_arrive_expect_tx(uint64_t *bar, uint32_t bytes)
 {
     asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)),
@@ -473,6 +484,8 @@ __device__ __forceinline__ uint32_t idesc_mx(int M, int N, uint32_t a, uint32_t 
            | (static_cast<uint32_t>(M >> 4) << 24)     // M / 16
            | (sf << 29);                               // byte of A's scale words
 }
+// The descriptor's bits of scale byte `sf`, to add to one made with sf = 0.
+__device__ __forceinline__ constexpr uint32_t idesc_mx_sf(uint32_t sf) { return (sf << 4) | (sf << 29); }
 constexpr uint32_t kMxf8f6f4E4M3 = 0, kMxf8f6f4E2M1 = 5, kMxf4E2M1 = 1;
 
 // Arrive once on the mbarrier at the same offset in each CTA of `cta_mask`
