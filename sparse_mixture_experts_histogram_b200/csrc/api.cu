@@ -1104,9 +1104,9 @@ static moe_status mx_gemm(MxGemmLaunch &a, void *ws, size_t ws_bytes, moe_stream
     a.err = reinterpret_cast<uint32_t *>(wsb);
     a.counters = wsb + kHeaderBytes;
     a.scratch = a.counters + align_up(mx_gemm_zero_bytes());
-    const moe_status st =
-        from_cuda(cudaMemsetAsync(wsb, 0, kHeaderBytes + mx_gemm_zero_bytes(), s));
+    const moe_status st = from_cuda(launch_clear(wsb, kHeaderBytes + mx_gemm_zero_bytes(), s));
     if (st != MOE_OK) return st;
+    a.pdl = true;
     return from_cuda(launch_mx_gemm(a, s));
 }
 

@@ -219,6 +219,7 @@ size_t mx_gemm_scratch_bytes(int S);
 size_t mx_gemm_zero_bytes();
 cudaError_t launch_rmsnorm(const NormLaunch &a, cudaStream_t s);
 cudaError_t launch_mx_quantize(const MxQuantLaunch &a, cudaStream_t s);
+cudaError_t launch_clear(void *p, size_t bytes, cudaStream_t s);  // 16-byte multiples
 cudaError_t launch_mx_gemm(const MxGemmLaunch &a, cudaStream_t s);
 
 // Failure-detection self-test (selftest.cu): a bounded wait that runs out.

@@ -59,7 +59,6 @@ constexpr int kMaxN = 192;               // token rows per tile
 constexpr uint32_t kRowBytes = 128;      // of an operand row in a stage
 constexpr uint32_t kATile = 128 * kRowBytes;
 constexpr int kChunkK = 512;             // values of K per scale chunk (16 scale bytes)
-constexpr int kScSlots = 4;              // scale chunks in shared memory
 constexpr uint32_t kScA = 128 * 16;      // bytes of a chunk's weight scales
 constexpr int kHalfK = 256;              // values of K per scale buffer in tensor memory
 constexpr int kWorkSlots = 4;            // units announced ahead by the scheduling warp
@@ -79,6 +78,11 @@ struct Shape {
     static constexpr uint32_t kStage = kATile + kBTile;
     static constexpr int kStages = NMAX == 192 ? 6 : NMAX == 96 ? 7 : 9;
     static constexpr uint32_t kScSlot = kScA + NMAX * 16;
+    static constexpr int kScSlots = NMAX == 32 ? 8 : 4;  // scale chunks in shared memory
+    // Few token rows: weights are read once, from HBM, whose latency the
+    // stages alone do not cover.  The warp that copies scales runs up to
+    // kScSlots chunks ahead and fetches the weights of its chunk into L2.
+    static constexpr bool kPrefetch = NMAX <= 96;
     // Tensor memory: two accumulators of NMAX columns, then kScBufs buffers
     // of the scales of 256 values of K.  128 values are one 32-bit word a
     // row: 4 columns of A's scales, then NMAX / 32 of B's.
@@ -195,7 +199,7 @@ struct Walk {
     int pair, pairs, units, whole, chunks;   // units [whole, units) may be cut
     int cutters;                             // pairs that share those: no range is empty
     int u;                                   // next whole unit
-    long long it, end, items;                // chunk items of the cut units
+    int it, end, items;                      // chunk items of the cut units (items pairs < 2^20)
     int first_cut;                           // the first cut unit of this pair
 
     // Units whole, whole + 1, .. hold `items` chunks of K; pair p < cutters
@@ -208,20 +212,17 @@ struct Walk {
         whole = whole_;
         chunks = chunks_;
         u = pair;
-        items = static_cast<long long>(units - whole) * chunks;
-        cutters = items < pairs ? static_cast<int>(items) : pairs;
-        it = end = 0;
+        items = (units - whole) * chunks;
+        cutters = items < pairs ? items : pairs;
+        it = end = first_cut = 0;
         if (pair < cutters) {
             it = items * pair / cutters;
             end = items * (pair + 1) / cutters;
+            first_cut = it / chunks;
         }
-        first_cut = static_cast<int>(it / chunks);
     }
 
-    __device__ __forceinline__ int owner(long long item) const
-    {
-        return static_cast<int>(((item + 1) * cutters - 1) / items);
-    }
+    __device__ __forceinline__ int owner(int item) const { return ((item + 1) * cutters - 1) / items; }
 
     // Next unit and its chunks; false when the pair is done.
     __device__ __forceinline__ bool next(Work &w, int &unit)
@@ -235,12 +236,12 @@ struct Walk {
             return true;
         }
         if (it >= end) return false;
-        const int c = static_cast<int>(it / chunks);
-        const long long base = static_cast<long long>(c) * chunks;
+        const int c = it / chunks;
+        const int base = c * chunks;
         unit = whole + c;
-        w.c0 = static_cast<int>(it - base);
-        const long long stop = base + chunks < end ? base + chunks : end;
-        w.c1 = static_cast<int>(stop - base);
+        w.c0 = it - base;
+        const int stop = base + chunks < end ? base + chunks : end;
+        w.c1 = stop - base;
         it = stop;
         w.part = -1;
         if (w.c0 != 0 || w.c1 != chunks) {
@@ -255,7 +256,7 @@ struct Walk {
     // The slot in which pair p stores its part of cut unit c.
     __device__ __forceinline__ int part_of(int p, int c) const
     {
-        return 2 * p + (static_cast<int>((items * p / cutters) / chunks) == c ? 0 : 1);
+        return 2 * p + (items * p / cutters / chunks == c ? 0 : 1);
     }
 };
 
@@ -319,15 +320,16 @@ __device__ __forceinline__ float gate_mul(float g, float b, int act)
     return __fdividef(act ? b : g * b, 1.0f + __expf(-g));
 }
 
-// 16 (bf16) accumulator columns of 32 lanes to rows t0 .. t0+15 of y: lane
+// NC accumulator columns of 32 lanes to rows t0 .. t0+NC-1 of y in bf16: lane
 // pairs swap so that each lane stores two neighbouring output columns.
-__device__ __forceinline__ void store_bf16(const GemmParams &p, const float (&v)[16], int row,
+template <int NC>
+__device__ __forceinline__ void store_bf16(const GemmParams &p, const float (&v)[NC], int row,
                                            int t0, int valid, int o, int lane)
 {
     const int odd = lane & 1;
     __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(p.y) + static_cast<size_t>(row + t0) * p.N + (o & ~1);
 #pragma unroll
-    for (int j = 0; j < 16; j += 2) {
+    for (int j = 0; j < NC; j += 2) {
         const float give = odd ? v[j] : v[j + 1];
         const float got = __shfl_xor_sync(0xffffffffu, give, 1);
         const __nv_bfloat162 b = odd ? __floats2bfloat162_rn(got, v[j + 1])
@@ -337,12 +339,13 @@ __device__ __forceinline__ void store_bf16(const GemmParams &p, const float (&v)
     }
 }
 
-__device__ __forceinline__ void store_fp32(const GemmParams &p, const float (&v)[16], int row,
+template <int NC>
+__device__ __forceinline__ void store_fp32(const GemmParams &p, const float (&v)[NC], int row,
                                            int t0, int valid, int o)
 {
     float *y = static_cast<float *>(p.y) + static_cast<size_t>(row + t0) * p.N + o;
 #pragma unroll
-    for (int j = 0; j < 16; ++j)
+    for (int j = 0; j < NC; ++j)
         if (o < p.N && t0 + j < valid) y[static_cast<size_t>(j) * p.N] = v[j];
 }
 
@@ -402,6 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mx_pair_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ CUtensorMap tmW3,
                    const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmS1,
                    const __grid_constant__ CUtensorMap tmS3, const __grid_constant__ CUtensorMap tmXs,
+                   const __grid_constant__ CUtensorMap tmP1, const __grid_constant__ CUtensorMap tmP3,
                    const GemmParams p)
 {
     using SM = Shape<NMAX>;
@@ -426,12 +430,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool leader = (cta == 0);
 
     uint8_t *scales = smem + kStages * SM::kStage;
-    float *xchg = reinterpret_cast<float *>(scales + kScSlots * SM::kScSlot);
+    float *xchg = reinterpret_cast<float *>(scales + SM::kScSlots * SM::kScSlot);
     uint64_t *full = reinterpret_cast<uint64_t *>(reinterpret_cast<uint8_t *>(xchg) + kXchg);
     uint64_t *empty = full + kStages;
-    uint64_t *cfull = empty + kStages;      // [kScSlots] scale chunk in shared memory
-    uint64_t *cempty = cfull + kScSlots;    // [kScSlots]
-    uint64_t *tfull = cempty + kScSlots;    // [2] accumulator
+    uint64_t *cfull = empty + kStages;      // [SM::kScSlots] scale chunk in shared memory
+    uint64_t *cempty = cfull + SM::kScSlots;    // [SM::kScSlots]
+    uint64_t *tfull = cempty + SM::kScSlots;    // [2] accumulator
     uint64_t *tempty = tfull + 2;           // [2]
     uint64_t *sfull = tempty + 2;           // [kScBufs] scales in tensor memory
     uint64_t *sempty = sfull + SM::kScBufs; // [kScBufs]
@@ -456,7 +460,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(&full[s], 1);
             ptx::mbar_init(&empty[s], 1);
         }
-        for (int s = 0; s < kScSlots; ++s) {
+        for (int s = 0; s < SM::kScSlots; ++s) {
             ptx::mbar_init(&cfull[s], 1);
             ptx::mbar_init(&cempty[s], 4);
         }
@@ -534,6 +538,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Both CTAs' barriers are initialised before either CTA signals the other.
     ptx::cluster_sync();
     ptx::tc_fence_after();
+    // Whatever follows may set itself up on SMs that this kernel leaves; it
+    // waits for the whole grid before it reads.
+    ptx::grid_dep_launch();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
     const int units = s_pre[E];
     const int pairs = static_cast<int>(gridDim.x >> 1);
@@ -618,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (issued & (1u << s)) drain_wait(&full[s], last_parity >> s & 1u);
     } else if (warp == 3) {
         // Copies of scales: few bytes in many short rows, so they take longer
-        // than a stage's operands; their own ring runs up to kScSlots chunks
+        // than a stage's operands; their own ring runs up to SM::kScSlots chunks
         // ahead.
         const bool one = ptx::elect_one();
         uint32_t slot = 0, cphase = 0, issued = 0, last_parity = 0;
@@ -636,17 +643,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::tma_load_2d(sc, &tmS1, &cfull[slot], c * 16, arow);
                     if (GATED) ptx::tma_load_2d(sc + kScA / 2, &tmS3, &cfull[slot], c * 16, arow);
                     ptx::tma_load_2d(sc + kScA, &tmXs, &cfull[slot], c * 16, w.r0);
+                    if (SM::kPrefetch) {
+                        ptx::tma_prefetch_2d(&tmP1, c * (kChunkK / 2), arow);
+                        if (GATED) ptx::tma_prefetch_2d(&tmP3, c * (kChunkK / 2), arow);
+                    }
                 }
                 issued |= 1u << slot;
                 last_parity = (last_parity & ~(1u << slot)) | cphase << slot;
-                if (++slot == kScSlots) {
+                if (++slot == SM::kScSlots) {
                     slot = 0;
                     cphase ^= 1u;
                 }
             }
         }
         if (one)
-            for (int s = 0; s < kScSlots; ++s)
+            for (int s = 0; s < SM::kScSlots; ++s)
                 if (issued & (1u << s)) drain_wait(&cfull[s], last_parity >> s & 1u);
     } else if (warp == 1) {
         if (leader) {
@@ -753,7 +764,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < kB; ++i) b[i] = src[128 + 32 * i + lane];
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(&cempty[slot]);
-                if (++slot == kScSlots) {
+                if (++slot == SM::kScSlots) {
                     slot = 0;
                     cphase ^= 1u;
                 }
@@ -859,8 +870,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float v[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
-                        if (p.y_type == kTypeBf16) store_bf16(p, v, w.r0, c * kColChunk, w.valid, o, lane);
-                        else store_fp32(p, v, w.r0, c * kColChunk, w.valid, o);
+                        if (p.y_type == kTypeBf16) store_bf16<16>(p, v, w.r0, c * kColChunk, w.valid, o, lane);
+                        else store_fp32<16>(p, v, w.r0, c * kColChunk, w.valid, o);
                     }
                 }
                 if (stop) break;
@@ -887,35 +898,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const uint32_t all = static_cast<uint32_t>(w.last - w.first + 1) * (GATED ? 2u : 1u);
                 if (seen + 1 == all) {
                     __threadfence();
+                    const float *base = p.parts + cta * pstep + lane + 32 * (GATED ? (q & 1) : q);
                     for (int c = half; c < nch; c += 2) {
-#pragma unroll
-                        for (int h8 = 0; h8 < 16; h8 += 8) {
+                        for (int h8 = 0; h8 < 16 && c * kColChunk + h8 < w.valid; h8 += 8) {
                             float v[8], u[8];
 #pragma unroll
                             for (int j = 0; j < 8; ++j) v[j] = u[j] = 0.0f;
-                            for (int pr = w.first; pr <= w.last; ++pr) {
-                                const float *src =
-                                    p.parts + (static_cast<size_t>(walk.part_of(pr, w.cut)) * 2 + cta) * pstep +
-                                    static_cast<size_t>(c * kColChunk + h8) * 128 + lane + 32 * (GATED ? (q & 1) : q);
+                            // four parts' loads in flight together
+                            for (int pr = w.first; pr <= w.last; pr += 4) {
+                                float a[4][8], b[4][8];
 #pragma unroll
-                                for (int j = 0; j < 8; ++j) {
-                                    v[j] += __ldcg(src + j * 128);
-                                    if (GATED) u[j] += __ldcg(src + j * 128 + 64);
+                                for (int g = 0; g < 4; ++g) {
+                                    const bool has = pr + g <= w.last;
+                                    const float *src =
+                                        base + static_cast<size_t>(has ? walk.part_of(pr + g, w.cut) : 0) * 2 * pstep +
+                                        static_cast<size_t>(c * kColChunk + h8) * 128;
+#pragma unroll
+                                    for (int j = 0; j < 8; ++j) {
+                                        a[g][j] = has ? __ldcg(src + j * 128) : 0.0f;
+                                        if (GATED) b[g][j] = has ? __ldcg(src + j * 128 + 64) : 0.0f;
+                                    }
                                 }
+#pragma unroll
+                                for (int g = 0; g < 4; ++g)
+#pragma unroll
+                                    for (int j = 0; j < 8; ++j) {
+                                        v[j] += a[g][j];
+                                        if (GATED) u[j] += b[g][j];
+                                    }
                             }
                             if constexpr (GATED) {
 #pragma unroll
                                 for (int j = 0; j < 8; ++j) v[j] = gate_mul(v[j], u[j], p.act);
                                 store_h8(p, v, w.r0, c * kColChunk + h8, w.valid, o, lane);
+                            } else if (p.y_type == kTypeBf16) {
+                                store_bf16<8>(p, v, w.r0, c * kColChunk + h8, w.valid, o, lane);
                             } else {
-                                // rows of this half chunk through the common stores
-                                float z[16];
-#pragma unroll
-                                for (int j = 0; j < 16; ++j) z[j] = j < 8 ? v[j] : 0.0f;
-                                const int t0 = c * kColChunk + h8;
-                                const int lim = t0 + 8 < w.valid ? t0 + 8 : w.valid;
-                                if (p.y_type == kTypeBf16) store_bf16(p, z, w.r0, t0, lim, o, lane);
-                                else store_fp32(p, z, w.r0, t0, lim, o);
+                                store_fp32<8>(p, v, w.r0, c * kColChunk + h8, w.valid, o);
                             }
                         }
                     }
@@ -924,7 +943,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     }
 
-    ptx::grid_dep_launch();
     ptx::tc_fence_before();
     __syncthreads();
     // Neither CTA may free tensor memory or exit while the other still
@@ -963,7 +981,7 @@ cudaError_t launch_t(const MxGemmLaunch &a, cudaStream_t s)
     const uint32_t abox = GATED ? 64 : 128;
     const int xbytes = FMT == kMxE4M3 ? a.K : a.K / 2;
     const int nsc = a.K / kMxBlock, wsc = mx_scale_pitch(a.K);
-    CUtensorMap tW1, tW3, tX, tS1, tS3, tXs;
+    CUtensorMap tW1, tW3, tX, tS1, tS3, tXs, tP1, tP3;
     auto weights = [&](CUtensorMap *m, const uint8_t *w) {
         return FMT == kMxE4M3 ? make_tmap_e2m1_wide(m, w, wrows, a.K, abox)
                               : make_tmap_rows(m, w, wrows, a.K / 2, a.K / 2, 128, abox);
@@ -977,6 +995,10 @@ cudaError_t launch_t(const MxGemmLaunch &a, cudaStream_t s)
         tW3 = tW1;
         tS3 = tS1;
     }
+    // For the fetches into L2: the packed bytes of a chunk.
+    if (e == cudaSuccess) e = make_tmap_rows(&tP1, a.W1, wrows, a.K / 2, a.K / 2, kChunkK / 2, abox);
+    if (e == cudaSuccess)
+        e = make_tmap_rows(&tP3, GATED ? a.W3 : a.W1, wrows, a.K / 2, a.K / 2, kChunkK / 2, abox);
     if (e == cudaSuccess) e = make_tmap_rows(&tX, a.x, a.S, xbytes, a.x_stride, 128, NMAX / 2);
     if (e == cudaSuccess) e = make_tmap_rows(&tXs, a.xs, a.S, nsc, a.xs_stride, 16, NMAX);
     if (e != cudaSuccess) return e;
@@ -1019,7 +1041,7 @@ cudaError_t launch_t(const MxGemmLaunch &a, cudaStream_t s)
     cfg.gridDim = dim3(2);
     cfg.gridDim = dim3(static_cast<unsigned>(2 * pair_count<FMT, GATED, NMAX>(cfg)));
     cfg.numAttrs = a.pdl ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, tW1, tW3, tX, tS1, tS3, tXs, p);
+    return cudaLaunchKernelEx(&cfg, kernel, tW1, tW3, tX, tS1, tS3, tXs, tP1, tP3, p);
 }
 
 template <int FMT, bool GATED>
@@ -1032,6 +1054,21 @@ cudaError_t launch_n(const MxGemmLaunch &a, cudaStream_t s)
 }
 
 }  // namespace
+
+// Zeroes the header and counters of a workspace ahead of a product.  A kernel
+// and not a memset, so that the product's set-up overlaps it.
+__global__ void __launch_bounds__(512) clear_kernel(uint4 *p, int n)
+{
+    ptx::grid_dep_launch();
+    ptx::grid_dep_wait();
+    for (int i = threadIdx.x; i < n; i += 512) p[i] = make_uint4(0u, 0u, 0u, 0u);
+}
+
+cudaError_t launch_clear(void *p, size_t bytes, cudaStream_t s)
+{
+    return launch_pdl(clear_kernel, dim3(1), dim3(512), 0, s, true, static_cast<uint4 *>(p),
+                      static_cast<int>(bytes / 16));
+}
 
 size_t mx_gemm_zero_bytes() { return kCounters * sizeof(uint32_t); }
 
