@@ -78,11 +78,7 @@ struct Shape {
     static constexpr uint32_t kStage = kATile + kBTile;
     static constexpr int kStages = NMAX == 192 ? 6 : NMAX == 96 ? 7 : 9;
     static constexpr uint32_t kScSlot = kScA + NMAX * 16;
-    static constexpr int kScSlots = NMAX == 32 ? 8 : 4;  // scale chunks in shared memory
-    // Few token rows: weights are read once, from HBM, whose latency the
-    // stages alone do not cover.  The warp that copies scales runs up to
-    // kScSlots chunks ahead and fetches the weights of its chunk into L2.
-    static constexpr bool kPrefetch = NMAX <= 96;
+    static constexpr int kScSlots = 4;  // scale chunks in shared memory
     // Tensor memory: two accumulators of NMAX columns, then kScBufs buffers
     // of the scales of 256 values of K.  128 values are one 32-bit word a
     // row: 4 columns of A's scales, then NMAX / 32 of B's.
@@ -114,37 +110,13 @@ struct GemmParams {
 };
 
 // ------------------------------------------------------------------ waiting
-__device__ __forceinline__ bool wait_cl(uint64_t *bar, uint32_t parity,
-                                        volatile uint32_t *abort_flag, uint32_t *gerr,
-                                        uint32_t code)
-{
-    if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
-    const uint64_t t0 = ptx::globaltimer();
-    for (uint32_t it = 1;; ++it) {
-        if (ptx::mbar_try_wait_cluster(bar, parity)) return true;
-        if (*abort_flag) return false;
-        if ((it & 63u) == 0 && ptx::globaltimer() - t0 > kWaitTimeoutNs) {
-            *abort_flag = 1u;
-            if (gerr) atomicOr(gerr, code);
-            return false;
-        }
-    }
-}
-
-__device__ __forceinline__ bool wait_cl_warp(uint64_t *bar, uint32_t parity,
-                                             volatile uint32_t *abort_flag, uint32_t *gerr,
-                                             uint32_t code)
-{
-    const bool ok = wait_cl(bar, parity, abort_flag, gerr, code);
-    const bool all = __all_sync(0xffffffffu, ok);
-    if (!all) *abort_flag = 1u;
-    return all;
-}
-
+// The bounded waits of common.cuh, whose acquire is at CTA scope: what the two
+// CTAs hand each other here is shared memory that copies fill and MMAs read,
+// and tensor memory, ordered by the tcgen05 fences.
 __device__ __forceinline__ void drain_wait(uint64_t *bar, uint32_t parity)
 {
     const uint64_t t0 = ptx::globaltimer();
-    while (!ptx::mbar_try_wait_cluster(bar, parity)) {
+    while (!ptx::mbar_try_wait(bar, parity)) {
         if (ptx::globaltimer() - t0 > 100000000ull) break;  // 100 ms
     }
 }
@@ -405,7 +377,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     mx_pair_kernel(const __grid_constant__ CUtensorMap tmW1, const __grid_constant__ CUtensorMap tmW3,
                    const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmS1,
                    const __grid_constant__ CUtensorMap tmS3, const __grid_constant__ CUtensorMap tmXs,
-                   const __grid_constant__ CUtensorMap tmP1, const __grid_constant__ CUtensorMap tmP3,
                    const GemmParams p)
 {
     using SM = Shape<NMAX>;
@@ -433,7 +404,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     float *xchg = reinterpret_cast<float *>(scales + SM::kScSlots * SM::kScSlot);
     uint64_t *full = reinterpret_cast<uint64_t *>(reinterpret_cast<uint8_t *>(xchg) + kXchg);
     uint64_t *empty = full + kStages;
-    uint64_t *cfull = empty + kStages;      // [SM::kScSlots] scale chunk in shared memory
+    uint64_t *cfull = empty + kStages;      // [kScSlots] scale chunk in shared memory
     uint64_t *cempty = cfull + SM::kScSlots;    // [SM::kScSlots]
     uint64_t *tfull = cempty + SM::kScSlots;    // [2] accumulator
     uint64_t *tempty = tfull + 2;           // [2]
@@ -555,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t wslot = 0, wphase = 0;
     Work w;
     auto next_unit = [&]() -> bool {
-        if (!wait_cl_warp(&wfull[wslot], wphase, abort_flag, p.err, kErrTimeoutEpi)) return false;
+        if (!bounded_wait_warp(&wfull[wslot], wphase, abort_flag, p.err, kErrTimeoutEpi)) return false;
         get(s_work + wslot * kWorkInts, w);
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&wempty[wslot]);
@@ -576,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 more = walk.next(w, unit);
                 if (more) place<NMAX>(w, unit, s_off, s_pre, E);
                 else w.e = -1;
-                if (!wait_cl(&wempty[wslot], wphase ^ 1u, abort_flag, p.err, kErrTimeoutEpi)) break;
+                if (!bounded_wait(&wempty[wslot], wphase ^ 1u, abort_flag, p.err, kErrTimeoutEpi)) break;
                 put(s_work + wslot * kWorkInts, w);
                 ptx::mbar_arrive(&wfull[wslot]);
                 if (++wslot == kWorkSlots) {
@@ -595,7 +566,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int brow = w.r0 + static_cast<int>(cta) * (w.n >> 1);
             const int k1 = min(w.c1 * kStagesPerChunk, ksteps);
             for (int ks = w.c0 * kStagesPerChunk; ks < k1; ++ks) {
-                if (!wait_cl_warp(&empty[stage], phase ^ 1u, abort_flag, p.err, kErrTimeoutMma)) {
+                if (!bounded_wait_warp(&empty[stage], phase ^ 1u, abort_flag, p.err, kErrTimeoutMma)) {
                     stop = true;
                     break;
                 }
@@ -625,7 +596,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 if (issued & (1u << s)) drain_wait(&full[s], last_parity >> s & 1u);
     } else if (warp == 3) {
         // Copies of scales: few bytes in many short rows, so they take longer
-        // than a stage's operands; their own ring runs up to SM::kScSlots chunks
+        // than a stage's operands; their own ring runs up to kScSlots chunks
         // ahead.
         const bool one = ptx::elect_one();
         uint32_t slot = 0, cphase = 0, issued = 0, last_parity = 0;
@@ -633,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         while (!stop && next_unit()) {
             const int arow = w.e * p.N + w.blk * p.rows_blk + static_cast<int>(cta) * (p.rows_blk / 2);
             for (int c = w.c0; c < w.c1; ++c) {
-                if (!wait_cl_warp(&cempty[slot], cphase ^ 1u, abort_flag, p.err, kErrTimeoutTma)) {
+                if (!bounded_wait_warp(&cempty[slot], cphase ^ 1u, abort_flag, p.err, kErrTimeoutTma)) {
                     stop = true;
                     break;
                 }
@@ -643,10 +614,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::tma_load_2d(sc, &tmS1, &cfull[slot], c * 16, arow);
                     if (GATED) ptx::tma_load_2d(sc + kScA / 2, &tmS3, &cfull[slot], c * 16, arow);
                     ptx::tma_load_2d(sc + kScA, &tmXs, &cfull[slot], c * 16, w.r0);
-                    if (SM::kPrefetch) {
-                        ptx::tma_prefetch_2d(&tmP1, c * (kChunkK / 2), arow);
-                        if (GATED) ptx::tma_prefetch_2d(&tmP3, c * (kChunkK / 2), arow);
-                    }
                 }
                 issued |= 1u << slot;
                 last_parity = (last_parity & ~(1u << slot)) | cphase << slot;
@@ -673,14 +640,14 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (uint32_t i = 0; !stop && next_unit(); ++i) {
                 const uint32_t buf = i & 1u;
                 const uint32_t idesc = ptx::idesc_mx(256, w.n, fmt_a, fmt_b, 0);
-                if (!wait_cl_warp(&tempty[buf], ((i >> 1) & 1u) ^ 1u, abort_flag, p.err, kErrTimeoutEpi))
+                if (!bounded_wait_warp(&tempty[buf], ((i >> 1) & 1u) ^ 1u, abort_flag, p.err, kErrTimeoutEpi))
                     break;
                 ptx::tc_fence_after();
                 const uint32_t dacc = tmem + buf * NMAX;
                 uint32_t acc = 0;
                 const int h1 = min(2 * w.c1, halves);
                 for (int h = 2 * w.c0; h < h1 && !stop; ++h) {
-                    if (!wait_cl_warp(&sfull[sb], sphase, abort_flag, p.err, kErrTimeoutTma)) {
+                    if (!bounded_wait_warp(&sfull[sb], sphase, abort_flag, p.err, kErrTimeoutTma)) {
                         stop = true;
                         break;
                     }
@@ -688,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int j = 0; j < kStagesPerHalf; ++j) {
                         if (h * kStagesPerHalf + j >= ksteps) break;
-                        if (!wait_cl_warp(&full[stage], phase, abort_flag, p.err, kErrTimeoutTma)) {
+                        if (!bounded_wait_warp(&full[stage], phase, abort_flag, p.err, kErrTimeoutTma)) {
                             stop = true;
                             break;
                         }
@@ -752,7 +719,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool stop = false;
         while (!stop && next_unit()) {
             for (int c = w.c0; c < w.c1 && !stop; ++c) {
-                if (!wait_cl_warp(&cfull[slot], cphase, abort_flag, p.err, kErrTimeoutTma)) {
+                if (!bounded_wait_warp(&cfull[slot], cphase, abort_flag, p.err, kErrTimeoutTma)) {
                     stop = true;
                     break;
                 }
@@ -771,7 +738,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     if (2 * c + h >= halves) break;
-                    if (!wait_cl_warp(&sempty[sb], sphase ^ 1u, abort_flag, p.err, kErrTimeoutMma)) {
+                    if (!bounded_wait_warp(&sempty[sb], sphase ^ 1u, abort_flag, p.err, kErrTimeoutMma)) {
                         stop = true;
                         break;
                     }
@@ -817,7 +784,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool stop = false;
         for (uint32_t i = 0; !stop && next_unit(); ++i) {
             const uint32_t buf = i & 1u;
-            if (!wait_cl_warp(&tfull[buf], (i >> 1) & 1u, abort_flag, p.err, kErrTimeoutMma)) break;
+            if (!bounded_wait_warp(&tfull[buf], (i >> 1) & 1u, abort_flag, p.err, kErrTimeoutMma)) break;
             ptx::tc_fence_after();
             const uint32_t tb = tmem + lane_base + buf * NMAX;
             const int nch = w.n / kColChunk;
@@ -981,7 +948,7 @@ cudaError_t launch_t(const MxGemmLaunch &a, cudaStream_t s)
     const uint32_t abox = GATED ? 64 : 128;
     const int xbytes = FMT == kMxE4M3 ? a.K : a.K / 2;
     const int nsc = a.K / kMxBlock, wsc = mx_scale_pitch(a.K);
-    CUtensorMap tW1, tW3, tX, tS1, tS3, tXs, tP1, tP3;
+    CUtensorMap tW1, tW3, tX, tS1, tS3, tXs;
     auto weights = [&](CUtensorMap *m, const uint8_t *w) {
         return FMT == kMxE4M3 ? make_tmap_e2m1_wide(m, w, wrows, a.K, abox)
                               : make_tmap_rows(m, w, wrows, a.K / 2, a.K / 2, 128, abox);
@@ -995,10 +962,6 @@ cudaError_t launch_t(const MxGemmLaunch &a, cudaStream_t s)
         tW3 = tW1;
         tS3 = tS1;
     }
-    // For the fetches into L2: the packed bytes of a chunk.
-    if (e == cudaSuccess) e = make_tmap_rows(&tP1, a.W1, wrows, a.K / 2, a.K / 2, kChunkK / 2, abox);
-    if (e == cudaSuccess)
-        e = make_tmap_rows(&tP3, GATED ? a.W3 : a.W1, wrows, a.K / 2, a.K / 2, kChunkK / 2, abox);
     if (e == cudaSuccess) e = make_tmap_rows(&tX, a.x, a.S, xbytes, a.x_stride, 128, NMAX / 2);
     if (e == cudaSuccess) e = make_tmap_rows(&tXs, a.xs, a.S, nsc, a.xs_stride, 16, NMAX);
     if (e != cudaSuccess) return e;
@@ -1041,7 +1004,7 @@ cudaError_t launch_t(const MxGemmLaunch &a, cudaStream_t s)
     cfg.gridDim = dim3(2);
     cfg.gridDim = dim3(static_cast<unsigned>(2 * pair_count<FMT, GATED, NMAX>(cfg)));
     cfg.numAttrs = a.pdl ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kernel, tW1, tW3, tX, tS1, tS3, tXs, tP1, tP3, p);
+    return cudaLaunchKernelEx(&cfg, kernel, tW1, tW3, tX, tS1, tS3, tXs, p);
 }
 
 template <int FMT, bool GATED>

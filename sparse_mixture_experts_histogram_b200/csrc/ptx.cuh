@@ -109,15 +109,6 @@ __device__ __forceinline__ void tma_load_2d_hint(void *dst, const CUtensorMap *m
         : "memory");
 }
 
-// Fetches one box of a 2-D tensor into L2.
-__device__ __forceinline__ void tma_prefetch_2d(const CUtensorMap *map, int32_t c0, int32_t c1)
-{
-    asm volatile("cp.async.bulk.prefetch.tensor.2d.L2.global.tile [%0, {%1, %2}];" ::"l"(
-                     reinterpret_cast<uint64_t>(map)),
-                 "r"(c0), "r"(c1)
-                 : "memory");
-}
-
 // Four rows r0..r3 (any order, any rows) of a 2-D tensor, columns c0.. of
 // the map's one-row box, to dst as rows 0..3 (tile::gather4; the tensor map's
 // box must be one row high).  Completes on `bar` like tma_load_2d.
