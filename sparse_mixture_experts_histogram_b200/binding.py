@@ -74,6 +74,8 @@ _L, _F = ctypes.c_longlong, ctypes.c_float
 def load_library(path: str | None = None) -> ctypes.CDLL:
     """Load ``libmoe_b200.so`` (built in-tree by ``build.py``)."""
     global _lib
+    if _lib is not None:  # loaded once, never replaced
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -142,7 +144,9 @@ def _ptr(t) -> int | None:
 def _stream(stream) -> int | None:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        # the current stream's handle without a Stream object around it
+        # (0.2 us instead of 3.4 us a call)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

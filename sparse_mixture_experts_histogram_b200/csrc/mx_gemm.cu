@@ -56,7 +56,7 @@ namespace {
 constexpr int kThreads = 512;
 constexpr int kEpiWarps = 8;
 constexpr int kMaxN = 192;               // token rows per tile
-constexpr uint32_t kRowBytes = 128;      // of an operand row in a stage
+constexpr uint32_t kRowBytes = 128;      // of an operand row in shared memory
 constexpr uint32_t kATile = 128 * kRowBytes;
 constexpr int kChunkK = 512;             // values of K per scale chunk (16 scale bytes)
 constexpr uint32_t kScA = 128 * 16;      // bytes of a chunk's weight scales
@@ -75,28 +75,37 @@ constexpr size_t kCounters = static_cast<size_t>(kMaxPairs) * 2 * kEpiWarps;
 template <int NMAX>
 struct Shape {
     static constexpr uint32_t kBTile = NMAX / 2 * kRowBytes;
-    static constexpr uint32_t kStage = kATile + kBTile;
-    static constexpr int kStages = NMAX == 192 ? 6 : NMAX == 96 ? 7 : 9;
+    static constexpr int kAtoms = NMAX == 192 ? 1 : 2;  // 128-byte columns per stage
+    static constexpr uint32_t kStage = kAtoms * (kATile + kBTile);
+    static constexpr int kStages = NMAX == 192 ? 6 : NMAX == 96 ? 4 : 5;
     static constexpr uint32_t kScSlot = kScA + NMAX * 16;
     static constexpr int kScSlots = 4;  // scale chunks in shared memory
-    // Tensor memory: two accumulators of NMAX columns, then kScBufs buffers
-    // of the scales of 256 values of K.  128 values are one 32-bit word a
-    // row: 4 columns of A's scales, then NMAX / 32 of B's.
+    // Tensor memory: kAccs accumulators of NMAX columns (four where they
+    // fit: short units then overlap the latency of several epilogues), then
+    // kScBufs buffers of the scales of 256 values of K.  128 values are one
+    // 32-bit word a row: 4 columns of A's scales, then NMAX / 32 of B's.
+    static constexpr int kAccs = NMAX == 192 ? 2 : 4;
     static constexpr uint32_t kWord = NMAX == 192 ? 12 : 8;
-    static constexpr uint32_t kScCol = 2 * NMAX;
+    static constexpr uint32_t kScCol = kAccs * NMAX;
     static constexpr int kScBufs = NMAX == 192 ? 5 : 8;
     static_assert(kScCol + kScBufs * 2 * kWord <= kTmemCols, "tensor memory");
-    static constexpr int kBarriers = 2 * kStages + 2 * kScSlots + 2 * 2 + 2 * kScBufs +
+    static constexpr int kBarriers = 2 * kStages + 2 * kScSlots + 2 * kAccs + 2 * kScBufs +
                                      2 * kWorkSlots + 1 + 8;
     static constexpr size_t kBytes = 1024 /* alignment slack */ + kStages * kStage +
                                      kScSlots * kScSlot + kXchg + kBarriers * 8 + 64 +
                                      kWorkSlots * kWorkInts * 4 + 2 * (kMaxE + 1) * sizeof(int32_t);
     static_assert(kBytes <= 227 * 1024, "shared memory");
     static_assert(kBTile % 1024 == 0, "swizzle atom");
+    // Rows per copy of x and of its scales.  A copy that reaches beyond the
+    // last row of x is slow (2 rows of 14336 e4m3 values in copies of 16: 30
+    // us a product, 24 us without), so few token rows come in small copies.
+    static constexpr int kXBox = NMAX == 32 ? 8 : NMAX / 2;
+    static constexpr int kXsBox = NMAX == 32 ? 16 : NMAX;
 };
 
 struct GemmParams {
     int S, K, E, N;
+    int xbox, xsbox;         // rows per copy of x and its scales
     int rows_blk;            // output columns per unit: 256, or 128 (gated)
     int act, y_type;
     const int32_t *offsets;  // [E+1] or nullptr
@@ -129,7 +138,9 @@ __device__ __forceinline__ int ceil16(int v) { return (v + 15) & ~15; }
 // the pairs that hold the unit's parts, `cut` the unit's number among those
 // that may be cut.
 struct Work {
-    int e, blk, r0, valid, n;
+    int e, blk;
+    int r0, n;               // the tile's n columns are the rows r0 ..
+    int lo, hi;              // of which columns lo .. hi-1 are the unit's
     int c0, c1;
     int part, first, last, cut;
 };
@@ -140,8 +151,9 @@ __device__ __forceinline__ void put(volatile int32_t *s, const Work &w)
     s[0] = w.e;
     s[1] = w.blk;
     s[2] = w.r0;
-    s[3] = w.valid;
+    s[3] = w.lo;
     s[4] = w.n;
+    s[11] = w.hi;
     s[5] = w.c0;
     s[6] = w.c1;
     s[7] = w.part;
@@ -156,7 +168,8 @@ __device__ __forceinline__ void get(const int32_t *s, Work &w)
     w.e = __shfl_sync(0xffffffffu, v, 0);
     w.blk = __shfl_sync(0xffffffffu, v, 1);
     w.r0 = __shfl_sync(0xffffffffu, v, 2);
-    w.valid = __shfl_sync(0xffffffffu, v, 3);
+    w.lo = __shfl_sync(0xffffffffu, v, 3);
+    w.hi = __shfl_sync(0xffffffffu, v, 11);
     w.n = __shfl_sync(0xffffffffu, v, 4);
     w.c0 = __shfl_sync(0xffffffffu, v, 5);
     w.c1 = __shfl_sync(0xffffffffu, v, 6);
@@ -254,7 +267,7 @@ __device__ __forceinline__ int seg_tiles(int cnt) { return (cnt + NMAX - 1) / NM
 // (neighbouring pairs share weights, and the tiles of an expert stay in L2).
 template <int NMAX>
 __device__ __forceinline__ void place(Work &w, int u, const int32_t *s_off, const int32_t *s_pre,
-                                      int E)
+                                      int E, int S)
 {
     int lo = 0, hi = E - 1;
     while (lo < hi) {  // largest e with pre[e] <= u
@@ -269,10 +282,14 @@ __device__ __forceinline__ void place(Work &w, int u, const int32_t *s_off, cons
     const int q = ceil16((cnt + nt - 1) / nt);
     w.blk = local / nt;
     const int t = local - w.blk * nt;
-    w.r0 = s_off[lo] + t * q;
+    const int first = s_off[lo] + t * q;
     const int rem = cnt - t * q;
-    w.valid = rem < q ? rem : q;
-    w.n = w.valid > 0 ? ceil16(w.valid) : 16;
+    const int valid = rem < 0 ? 0 : rem < q ? rem : q;
+    w.n = valid > 0 ? ceil16(valid) : 16;
+    // The n columns start earlier where they would reach beyond the last row.
+    w.r0 = min(first, max(0, S - w.n));
+    w.lo = first - w.r0;
+    w.hi = w.lo + valid;
 }
 
 __device__ __forceinline__ int warp_scan_incl(int v, int lane)
@@ -296,7 +313,7 @@ __device__ __forceinline__ float gate_mul(float g, float b, int act)
 // pairs swap so that each lane stores two neighbouring output columns.
 template <int NC>
 __device__ __forceinline__ void store_bf16(const GemmParams &p, const float (&v)[NC], int row,
-                                           int t0, int valid, int o, int lane)
+                                           int t0, int lo, int hi, int o, int lane)
 {
     const int odd = lane & 1;
     __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(p.y) + static_cast<size_t>(row + t0) * p.N + (o & ~1);
@@ -306,25 +323,25 @@ __device__ __forceinline__ void store_bf16(const GemmParams &p, const float (&v)
         const float got = __shfl_xor_sync(0xffffffffu, give, 1);
         const __nv_bfloat162 b = odd ? __floats2bfloat162_rn(got, v[j + 1])
                                      : __floats2bfloat162_rn(v[j], got);
-        if (o < p.N && t0 + j + odd < valid)
+        if (o < p.N && t0 + j + odd >= lo && t0 + j + odd < hi)
             *reinterpret_cast<__nv_bfloat162 *>(y + static_cast<size_t>(j + odd) * p.N) = b;
     }
 }
 
 template <int NC>
 __device__ __forceinline__ void store_fp32(const GemmParams &p, const float (&v)[NC], int row,
-                                           int t0, int valid, int o)
+                                           int t0, int lo, int hi, int o)
 {
     float *y = static_cast<float *>(p.y) + static_cast<size_t>(row + t0) * p.N + o;
 #pragma unroll
     for (int j = 0; j < NC; ++j)
-        if (o < p.N && t0 + j < valid) y[static_cast<size_t>(j) * p.N] = v[j];
+        if (o < p.N && t0 + j >= lo && t0 + j < hi) y[static_cast<size_t>(j) * p.N] = v[j];
 }
 
 // Eight tokens of h at 32 columns f (one per lane): bf16, or e4m3 with the
 // scale of the 32 lanes.
 __device__ __forceinline__ void store_h8(const GemmParams &p, const float (&v)[8], int row, int t0,
-                                         int valid, int f, int lane)
+                                         int lo, int hi, int f, int lane)
 {
     if (p.y != nullptr) {
         const int odd = lane & 1;
@@ -335,7 +352,7 @@ __device__ __forceinline__ void store_h8(const GemmParams &p, const float (&v)[8
             const float got = __shfl_xor_sync(0xffffffffu, give, 1);
             const __nv_bfloat162 b = odd ? __floats2bfloat162_rn(got, v[j + 1])
                                          : __floats2bfloat162_rn(v[j], got);
-            if (t0 + j + odd < valid)
+            if (t0 + j + odd >= lo && t0 + j + odd < hi)
                 *reinterpret_cast<__nv_bfloat162 *>(y + static_cast<size_t>(j + odd) * p.N) = b;
         }
         return;
@@ -350,7 +367,7 @@ __device__ __forceinline__ void store_h8(const GemmParams &p, const float (&v)[8
             c == 255u ? 0u : __nv_cvt_float_to_fp8(v[j] * mx_inv_scale(c), __NV_SATFINITE, __NV_E4M3);
         w[j >> 2] |= code << (8 * (j & 3));
     }
-    if (lane < 8 && t0 + lane < valid) {
+    if (lane < 8 && t0 + lane >= lo && t0 + lane < hi) {
         uint8_t *s = p.qs + static_cast<size_t>(row + t0 + lane) * p.qpitch;
         s[f >> 5] = static_cast<uint8_t>(mine);
         if ((f >> 5) == (p.N >> 5) - 1)
@@ -366,7 +383,7 @@ __device__ __forceinline__ void store_h8(const GemmParams &p, const float (&v)[8
         b = __shfl_xor_sync(0xffffffffu, a, 2);
         a = (lane & 2) ? __byte_perm(a, b, 0x3276) : __byte_perm(a, b, 0x5410);
         const int t = t0 + 4 * g + (lane & 3);
-        if (t < valid)
+        if (t >= lo && t < hi)
             *reinterpret_cast<uint32_t *>(p.q + static_cast<size_t>(row + t) * p.N + (f & ~3)) = a;
     }
 }
@@ -381,12 +398,16 @@ __global__ void __launch_bounds__(kThreads, 1)
 {
     using SM = Shape<NMAX>;
     constexpr int kStages = SM::kStages;
-    constexpr int kStageK = FMT == kMxE4M3 ? 128 : 256;      // values of K per stage
-    constexpr int kStagesPerChunk = kChunkK / kStageK;
-    constexpr int kStagesPerHalf = kHalfK / kStageK;
-    // Bytes a CTA's copies count per stage: a spread copy counts the 4-bit
-    // codes it moves, not the shared memory it covers.
-    constexpr uint32_t kStageTx = SM::kBTile + (FMT == kMxE4M3 ? kATile / 2 : kATile);
+    constexpr int kAtoms = SM::kAtoms;
+    constexpr int kAtomK = FMT == kMxE4M3 ? 128 : 256;  // values of K per atom
+    constexpr int kAtomsPerHalf = kHalfK / kAtomK;
+    // e4m3 rows: one copy spreads the weights of a stage's atoms, in groups of
+    // 8 rows: [group][atom][8 rows].  e2m1 rows: [atom][rows], a copy each.
+    constexpr uint32_t kAGroup = FMT == kMxE4M3 ? kAtoms * 1024 : 1024;
+    constexpr uint32_t kAAtom = FMT == kMxE4M3 ? 1024 : kATile;
+    constexpr bool kXSmall = FMT == kMxE4M3 && SM::kXBox == 8;
+    constexpr uint32_t kBGroup = kXSmall ? kAtoms * 1024 : 1024;
+    constexpr uint32_t kBAtom = kXSmall ? 1024 : SM::kBTile;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
@@ -406,9 +427,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *empty = full + kStages;
     uint64_t *cfull = empty + kStages;      // [kScSlots] scale chunk in shared memory
     uint64_t *cempty = cfull + SM::kScSlots;    // [SM::kScSlots]
-    uint64_t *tfull = cempty + SM::kScSlots;    // [2] accumulator
-    uint64_t *tempty = tfull + 2;           // [2]
-    uint64_t *sfull = tempty + 2;           // [kScBufs] scales in tensor memory
+    uint64_t *tfull = cempty + SM::kScSlots;  // [kAccs] accumulator
+    uint64_t *tempty = tfull + SM::kAccs;   // [kAccs]
+    uint64_t *sfull = tempty + SM::kAccs;   // [kScBufs] scales in tensor memory
     uint64_t *sempty = sfull + SM::kScBufs; // [kScBufs]
     uint64_t *wfull = sempty + SM::kScBufs; // [kWorkSlots] unit announced
     uint64_t *wempty = wfull + kWorkSlots;  // [kWorkSlots]
@@ -423,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int E = p.offsets ? p.E : 1;
     const int blocks = (p.N + p.rows_blk - 1) / p.rows_blk;
     const int chunks = (p.K + kChunkK - 1) / kChunkK;
-    const int ksteps = (p.K + kStageK - 1) / kStageK;
+    const int atoms = (p.K + kAtomK - 1) / kAtomK;
     const int halves = (p.K + kHalfK - 1) / kHalfK;
 
     if (threadIdx.x == 0) {
@@ -435,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(&cfull[s], 1);
             ptx::mbar_init(&cempty[s], 4);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < SM::kAccs; ++b) {
             ptx::mbar_init(&tfull[b], 1);
             ptx::mbar_init(&tempty[b], 2 * kEpiWarps);
         }
@@ -504,6 +525,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (lane == 31) s_pre[E] = incl;
     }
+    // The scheduling warp decodes the pair's first unit before the barrier.
+    Work w;
+    Walk walk;
+    bool more = false;
+    const int pairs = static_cast<int>(gridDim.x >> 1);
+    if (warp == 2) {
+        __syncwarp();
+        const int units = s_pre[E];
+        walk.start(static_cast<int>(blockIdx.x >> 1), pairs, units, plan(units, pairs, chunks), chunks);
+        if (lane == 0) {
+            int unit = 0;
+            more = walk.next(w, unit);
+            if (more) place<NMAX>(w, unit, s_off, s_pre, E, p.S);
+        }
+    }
     ptx::tc_fence_before();
     __syncthreads();
     // Both CTAs' barriers are initialised before either CTA signals the other.
@@ -513,10 +549,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // waits for the whole grid before it reads.
     ptx::grid_dep_launch();
     const uint32_t tmem = __shfl_sync(0xffffffffu, *tmem_slot, 0);
-    const int units = s_pre[E];
-    const int pairs = static_cast<int>(gridDim.x >> 1);
-    const int whole = plan(units, pairs, chunks);
-
     // Shared::cluster addresses of the even CTA's barriers.
     const uint32_t full0 = ptx::mapa_shared(ptx::smem_addr(full), 0);
     const uint32_t tempty0 = ptx::mapa_shared(ptx::smem_addr(tempty), 0);
@@ -524,7 +556,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     // Takes the next announced unit; false at the end (or after a failure).
     uint32_t wslot = 0, wphase = 0;
-    Work w;
     auto next_unit = [&]() -> bool {
         if (!bounded_wait_warp(&wfull[wslot], wphase, abort_flag, p.err, kErrTimeoutEpi)) return false;
         get(s_work + wslot * kWorkInts, w);
@@ -539,14 +570,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 2) {
         // Scheduling: decodes the pair's units ahead of the other roles.
         if (lane == 0) {
-            Walk walk;
-            walk.start(static_cast<int>(blockIdx.x >> 1), pairs, units, whole, chunks);
-            bool more = true;
-            while (more) {
-                int unit = 0;
-                more = walk.next(w, unit);
-                if (more) place<NMAX>(w, unit, s_off, s_pre, E);
-                else w.e = -1;
+            while (true) {
+                if (!more) w.e = -1;
                 if (!bounded_wait(&wempty[wslot], wphase ^ 1u, abort_flag, p.err, kErrTimeoutEpi)) break;
                 put(s_work + wslot * kWorkInts, w);
                 ptx::mbar_arrive(&wfull[wslot]);
@@ -554,6 +579,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     wslot = 0;
                     wphase ^= 1u;
                 }
+                if (!more) break;
+                int unit = 0;
+                more = walk.next(w, unit);
+                if (more) place<NMAX>(w, unit, s_off, s_pre, E, p.S);
             }
         }
     } else if (warp == 0) {
@@ -563,9 +592,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool stop = false;
         while (!stop && next_unit()) {
             const int arow = w.e * p.N + w.blk * p.rows_blk + static_cast<int>(cta) * (p.rows_blk / 2);
-            const int brow = w.r0 + static_cast<int>(cta) * (w.n >> 1);
-            const int k1 = min(w.c1 * kStagesPerChunk, ksteps);
-            for (int ks = w.c0 * kStagesPerChunk; ks < k1; ++ks) {
+            const int half = w.n >> 1;
+            const int brow = w.r0 + static_cast<int>(cta) * half;
+            // Copies of x per CTA and their bytes per atom; with fewer rows
+            // than a copy would hold, the odd CTA has none.
+            const bool few = p.xbox < SM::kXBox;
+            const int nx = NMAX == 32 ? (few ? 1 - static_cast<int>(cta) : half / SM::kXBox) : 1;
+            const uint32_t tx = 2 * kAtoms * (FMT == kMxE4M3 ? kATile / 2 : kATile) +
+                                kAtoms * kRowBytes * (few ? p.xbox : 2 * SM::kXBox * (NMAX == 32 ? half / SM::kXBox : 1));
+            const int a1 = min(w.c1 * 2 * kAtomsPerHalf, atoms);
+            for (int a = w.c0 * 2 * kAtomsPerHalf; a < a1; a += kAtoms) {
                 if (!bounded_wait_warp(&empty[stage], phase ^ 1u, abort_flag, p.err, kErrTimeoutMma)) {
                     stop = true;
                     break;
@@ -573,12 +609,33 @@ __global__ void __launch_bounds__(kThreads, 1)
                 uint8_t *sa = smem + stage * SM::kStage;
                 const uint32_t fb = full0 + 8 * stage;
                 if (one) {
-                    if (leader) ptx::mbar_arrive_expect_tx(&full[stage], 2 * kStageTx);
-                    // 128 bytes of a row in shared memory: the coordinate
-                    // counts codes (the spread copy) or bytes
-                    ptx::tma_load_2d_pair(sa, &tmW1, fb, ks * 128, arow, pol);
-                    if (GATED) ptx::tma_load_2d_pair(sa + kATile / 2, &tmW3, fb, ks * 128, arow, pol);
-                    ptx::tma_load_2d_pair(sa + kATile, &tmX, fb, ks * 128, brow, pol);
+                    if (leader) ptx::mbar_arrive_expect_tx(&full[stage], tx);
+                    // (a spread copy counts the 4-bit codes it moves, not the
+                    // shared memory it covers)
+                    if constexpr (FMT == kMxE4M3) {
+                        ptx::tma_load_4d_pair(sa, &tmW1, fb, 0, 0, a, arow >> 3, pol);
+                        if (GATED)
+                            ptx::tma_load_4d_pair(sa + kAtoms * kATile / 2, &tmW3, fb, 0, 0, a, arow >> 3, pol);
+                        // [copy][atom][rows]: 8 rows a copy are a swizzle group
+                        if (few) {
+                            for (int t = 0; t < nx * kAtoms; ++t)
+                                ptx::tma_load_3d_pair(sa + kAtoms * kATile + t * kBAtom, &tmX, fb, 0, brow, a + t, pol);
+                        } else {
+                            for (int x = 0; x < nx; ++x)
+                                ptx::tma_load_3d_pair(sa + kAtoms * (kATile + x * SM::kXBox * kRowBytes), &tmX, fb, 0,
+                                                      brow + x * SM::kXBox, a, pol);
+                        }
+                    } else {
+#pragma unroll
+                        for (int t = 0; t < kAtoms; ++t) {
+                            uint8_t *at = sa + t * kATile;
+                            ptx::tma_load_2d_pair(at, &tmW1, fb, (a + t) * 128, arow, pol);
+                            if (GATED) ptx::tma_load_2d_pair(at + kATile / 2, &tmW3, fb, (a + t) * 128, arow, pol);
+                            for (int x = 0; x < nx; ++x)
+                                ptx::tma_load_2d_pair(sa + kAtoms * kATile + t * SM::kBTile + x * SM::kXBox * kRowBytes,
+                                                      &tmX, fb, (a + t) * 128, brow + x * SM::kXBox, pol);
+                        }
+                    }
                 }
                 issued |= 1u << stage;
                 last_parity = (last_parity & ~(1u << stage)) | phase << stage;
@@ -603,6 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         bool stop = false;
         while (!stop && next_unit()) {
             const int arow = w.e * p.N + w.blk * p.rows_blk + static_cast<int>(cta) * (p.rows_blk / 2);
+            const int ns = p.xsbox < SM::kXsBox ? 1 : (w.n + SM::kXsBox - 1) / SM::kXsBox;
             for (int c = w.c0; c < w.c1; ++c) {
                 if (!bounded_wait_warp(&cempty[slot], cphase ^ 1u, abort_flag, p.err, kErrTimeoutTma)) {
                     stop = true;
@@ -610,10 +668,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 uint8_t *sc = scales + slot * SM::kScSlot;
                 if (one) {
-                    ptx::mbar_arrive_expect_tx(&cfull[slot], SM::kScSlot);
+                    ptx::mbar_arrive_expect_tx(&cfull[slot], kScA + ns * p.xsbox * 16);
                     ptx::tma_load_2d(sc, &tmS1, &cfull[slot], c * 16, arow);
                     if (GATED) ptx::tma_load_2d(sc + kScA / 2, &tmS3, &cfull[slot], c * 16, arow);
-                    ptx::tma_load_2d(sc + kScA, &tmXs, &cfull[slot], c * 16, w.r0);
+                    for (int x = 0; x < ns; ++x)
+                        ptx::tma_load_2d(sc + kScA + x * SM::kXsBox * 16, &tmXs, &cfull[slot], c * 16,
+                                         w.r0 + x * SM::kXsBox);
                 }
                 issued |= 1u << slot;
                 last_parity = (last_parity & ~(1u << slot)) | cphase << slot;
@@ -631,20 +691,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool one = ptx::elect_one();
             uint32_t stage = 0, phase = 0, sb = 0, sphase = 0;
             // Descriptors differ in their start address (16-byte units) only.
-            const uint64_t desc0 = ptx::sw128_kmajor_desc(0);
+            const uint64_t desc_a = ptx::sw128_kmajor_desc(0, kAGroup);
+            const uint64_t desc_b = ptx::sw128_kmajor_desc(0, kBGroup);
             const uint32_t smem16 = ptx::smem_addr(smem) >> 4;
             const uint32_t fmt_a = FMT == kMxE4M3 ? ptx::kMxf8f6f4E2M1 : ptx::kMxf4E2M1;
             const uint32_t fmt_b = FMT == kMxE4M3 ? ptx::kMxf8f6f4E4M3 : ptx::kMxf4E2M1;
-            const bool odd_end = p.K % kHalfK != 0;   // the last e2m1 stage holds 128 values of K
+            const bool odd_end = p.K % kHalfK != 0;   // the last 256 values of K are only 128
             bool stop = false;
             for (uint32_t i = 0; !stop && next_unit(); ++i) {
-                const uint32_t buf = i & 1u;
+                const uint32_t buf = i % SM::kAccs;
                 const uint32_t idesc = ptx::idesc_mx(256, w.n, fmt_a, fmt_b, 0);
-                if (!bounded_wait_warp(&tempty[buf], ((i >> 1) & 1u) ^ 1u, abort_flag, p.err, kErrTimeoutEpi))
+                if (!bounded_wait_warp(&tempty[buf], ((i / SM::kAccs) & 1u) ^ 1u, abort_flag, p.err, kErrTimeoutEpi))
                     break;
                 ptx::tc_fence_after();
                 const uint32_t dacc = tmem + buf * NMAX;
                 uint32_t acc = 0;
+                int in_stage = 0;  // atoms of the stage used so far
                 const int h1 = min(2 * w.c1, halves);
                 for (int h = 2 * w.c0; h < h1 && !stop; ++h) {
                     if (!bounded_wait_warp(&sfull[sb], sphase, abort_flag, p.err, kErrTimeoutTma)) {
@@ -653,16 +715,18 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                     const uint32_t word0 = tmem + SM::kScCol + sb * (2 * SM::kWord);
 #pragma unroll
-                    for (int j = 0; j < kStagesPerHalf; ++j) {
-                        if (h * kStagesPerHalf + j >= ksteps) break;
-                        if (!bounded_wait_warp(&full[stage], phase, abort_flag, p.err, kErrTimeoutTma)) {
+                    for (int j = 0; j < kAtomsPerHalf; ++j) {
+                        if (h * kAtomsPerHalf + j >= atoms) break;
+                        if (in_stage == 0 &&
+                            !bounded_wait_warp(&full[stage], phase, abort_flag, p.err, kErrTimeoutTma)) {
                             stop = true;
                             break;
                         }
                         ptx::tc_fence_after();
                         const uint32_t a16 = smem16 + stage * (SM::kStage >> 4);
-                        const uint64_t da = desc0 | a16;
-                        const uint64_t db = desc0 | (a16 + (kATile >> 4));
+                        const uint64_t da = desc_a | (a16 + in_stage * (kAAtom >> 4));
+                        const uint64_t db = desc_b | (a16 + ((kAtoms * kATile + in_stage * kBAtom) >> 4));
+                        const bool last = ++in_stage == kAtoms || h * kAtomsPerHalf + j + 1 == atoms;
                         if (one) {
                             if constexpr (FMT == kMxE4M3) {
                                 // 4 x 32 values, bytes 0..3 of one word
@@ -687,12 +751,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                               word0 + SM::kWord, word0 + SM::kWord + 4, 1u);
                                 }
                             }
-                            ptx::tc_commit_pair(&empty[stage], 0x3);
+                            if (last) ptx::tc_commit_pair(&empty[stage], 0x3);
                         }
                         acc = 1;
-                        if (++stage == static_cast<uint32_t>(kStages)) {
-                            stage = 0;
-                            phase ^= 1u;
+                        if (last) {
+                            in_stage = 0;
+                            if (++stage == static_cast<uint32_t>(kStages)) {
+                                stage = 0;
+                                phase ^= 1u;
+                            }
                         }
                     }
                     if (stop) break;
@@ -776,15 +843,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t lane_base = static_cast<uint32_t>(32 * q) << 16;
         const int wpair = (q & 1) + 2 * half;  // (a, b) warp pairs: quarters (0,2) and (1,3)
         const bool is_a = q < 2;               // lanes 0..63: W1 products (gated)
-        Walk walk;  // for the slots of other pairs' parts
-        walk.start(static_cast<int>(blockIdx.x >> 1), pairs, units, whole, chunks);
+        // for the slots of other pairs' parts
+        walk.start(static_cast<int>(blockIdx.x >> 1), pairs, s_pre[E], plan(s_pre[E], pairs, chunks), chunks);
         float *xa = xchg + wpair * (2 * 2 * 8 * 32);
         uint32_t xuse[2] = {0u, 0u};
         int xb = 0;
         bool stop = false;
         for (uint32_t i = 0; !stop && next_unit(); ++i) {
-            const uint32_t buf = i & 1u;
-            if (!bounded_wait_warp(&tfull[buf], (i >> 1) & 1u, abort_flag, p.err, kErrTimeoutMma)) break;
+            const uint32_t buf = i % SM::kAccs;
+            if (!bounded_wait_warp(&tfull[buf], (i / SM::kAccs) & 1u, abort_flag, p.err, kErrTimeoutMma)) break;
             ptx::tc_fence_after();
             const uint32_t tb = tmem + lane_base + buf * NMAX;
             const int nch = w.n / kColChunk;
@@ -831,14 +898,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                             const float b = is_a ? ot : __uint_as_float(r[8 + j]);
                             v[j] = gate_mul(g, b, p.act);
                         }
-                        store_h8(p, v, w.r0, c * kColChunk + (is_a ? 0 : 8), w.valid, o, lane);
+                        store_h8(p, v, w.r0, c * kColChunk + (is_a ? 0 : 8), w.lo, w.hi, o, lane);
                         xb ^= 1;
                     } else {
                         float v[16];
 #pragma unroll
                         for (int j = 0; j < 16; ++j) v[j] = __uint_as_float(r[j]);
-                        if (p.y_type == kTypeBf16) store_bf16<16>(p, v, w.r0, c * kColChunk, w.valid, o, lane);
-                        else store_fp32<16>(p, v, w.r0, c * kColChunk, w.valid, o);
+                        if (p.y_type == kTypeBf16) store_bf16<16>(p, v, w.r0, c * kColChunk, w.lo, w.hi, o, lane);
+                        else store_fp32<16>(p, v, w.r0, c * kColChunk, w.lo, w.hi, o);
                     }
                 }
                 if (stop) break;
@@ -867,7 +934,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     __threadfence();
                     const float *base = p.parts + cta * pstep + lane + 32 * (GATED ? (q & 1) : q);
                     for (int c = half; c < nch; c += 2) {
-                        for (int h8 = 0; h8 < 16 && c * kColChunk + h8 < w.valid; h8 += 8) {
+                        for (int h8 = 0; h8 < 16 && c * kColChunk + h8 < w.hi; h8 += 8) {
                             float v[8], u[8];
 #pragma unroll
                             for (int j = 0; j < 8; ++j) v[j] = u[j] = 0.0f;
@@ -897,11 +964,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                             if constexpr (GATED) {
 #pragma unroll
                                 for (int j = 0; j < 8; ++j) v[j] = gate_mul(v[j], u[j], p.act);
-                                store_h8(p, v, w.r0, c * kColChunk + h8, w.valid, o, lane);
+                                store_h8(p, v, w.r0, c * kColChunk + h8, w.lo, w.hi, o, lane);
                             } else if (p.y_type == kTypeBf16) {
-                                store_bf16<8>(p, v, w.r0, c * kColChunk + h8, w.valid, o, lane);
+                                store_bf16<8>(p, v, w.r0, c * kColChunk + h8, w.lo, w.hi, o, lane);
                             } else {
-                                store_fp32<8>(p, v, w.r0, c * kColChunk + h8, w.valid, o);
+                                store_fp32<8>(p, v, w.r0, c * kColChunk + h8, w.lo, w.hi, o);
                             }
                         }
                     }
@@ -922,7 +989,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     ptx::cluster_sync();
 }
 
-// Clusters of two that fit the device at a time, per kernel.
+// Clusters of two that fit the device at a time, per kernel (0: the kernel
+// cannot run here); the first call on a device also sets the kernel up.
 template <int FMT, bool GATED, int NMAX>
 int pair_count(cudaLaunchConfig_t &cfg)
 {
@@ -931,6 +999,10 @@ int pair_count(cudaLaunchConfig_t &cfg)
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) dev = 0;
     int n = known[dev].load(std::memory_order_relaxed);
     if (n > 0) return n;
+    const cudaError_t e = cudaFuncSetAttribute(mx_pair_kernel<FMT, GATED, NMAX>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(cfg.dynamicSmemBytes));
+    if (e != cudaSuccess) return 0;
     if (cudaOccupancyMaxActiveClusters(&n, mx_pair_kernel<FMT, GATED, NMAX>, &cfg) != cudaSuccess || n < 1)
         n = device_sm_count() / 2;
     n = std::max(1, std::min(n, kMaxPairs));
@@ -946,11 +1018,12 @@ cudaError_t launch_t(const MxGemmLaunch &a, cudaStream_t s)
     using SM = Shape<NMAX>;
     const uint64_t wrows = static_cast<uint64_t>(a.E) * a.N;
     const uint32_t abox = GATED ? 64 : 128;
-    const int xbytes = FMT == kMxE4M3 ? a.K : a.K / 2;
+    const int xbox = NMAX == 32 ? std::min(SM::kXBox, a.S) : SM::kXBox;
+    const int xsbox = NMAX == 32 ? std::min(SM::kXsBox, a.S) : SM::kXsBox;
     const int nsc = a.K / kMxBlock, wsc = mx_scale_pitch(a.K);
     CUtensorMap tW1, tW3, tX, tS1, tS3, tXs;
     auto weights = [&](CUtensorMap *m, const uint8_t *w) {
-        return FMT == kMxE4M3 ? make_tmap_e2m1_wide(m, w, wrows, a.K, abox)
+        return FMT == kMxE4M3 ? make_tmap_e2m1_wide(m, w, wrows, a.K, abox, SM::kAtoms)
                               : make_tmap_rows(m, w, wrows, a.K / 2, a.K / 2, 128, abox);
     };
     cudaError_t e = weights(&tW1, a.W1);
@@ -962,19 +1035,19 @@ cudaError_t launch_t(const MxGemmLaunch &a, cudaStream_t s)
         tW3 = tW1;
         tS3 = tS1;
     }
-    if (e == cudaSuccess) e = make_tmap_rows(&tX, a.x, a.S, xbytes, a.x_stride, 128, NMAX / 2);
-    if (e == cudaSuccess) e = make_tmap_rows(&tXs, a.xs, a.S, nsc, a.xs_stride, 16, NMAX);
+    if (e == cudaSuccess)
+        e = FMT == kMxE4M3 ? make_tmap_row_atoms(&tX, a.x, a.S, a.K, a.x_stride, xbox, xbox < SM::kXBox ? 1 : SM::kAtoms)
+                           : make_tmap_rows(&tX, a.x, a.S, a.K / 2, a.x_stride, 128, xbox);
+    if (e == cudaSuccess) e = make_tmap_rows(&tXs, a.xs, a.S, nsc, a.xs_stride, 16, xsbox);
     if (e != cudaSuccess) return e;
     auto *kernel = mx_pair_kernel<FMT, GATED, NMAX>;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(SM::kBytes));
-    if (e != cudaSuccess) return e;
-
     GemmParams p{};
     p.S = a.S;
     p.K = a.K;
     p.E = a.E;
     p.N = a.N;
+    p.xbox = xbox;
+    p.xsbox = xsbox;
     p.rows_blk = GATED ? 128 : 256;
     p.act = a.act;
     p.y_type = a.y_type;
@@ -1002,7 +1075,9 @@ cudaError_t launch_t(const MxGemmLaunch &a, cudaStream_t s)
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     cfg.gridDim = dim3(2);
-    cfg.gridDim = dim3(static_cast<unsigned>(2 * pair_count<FMT, GATED, NMAX>(cfg)));
+    const int pairs = pair_count<FMT, GATED, NMAX>(cfg);
+    if (pairs < 1) return cudaErrorInvalidConfiguration;
+    cfg.gridDim = dim3(static_cast<unsigned>(2 * pairs));
     cfg.numAttrs = a.pdl ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, tW1, tW3, tX, tS1, tS3, tXs, p);
 }

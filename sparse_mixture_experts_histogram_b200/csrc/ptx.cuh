@@ -275,13 +275,13 @@ __device__ __forceinline__ void tc_mma_f16_ts(uint32_t d_tmem, uint32_t a_tmem, 
 
 // Shared-memory matrix descriptor of a K-major operand tile written by TMA
 // with 128-byte swizzling: rows of 128 bytes (64 bf16 of K), groups of 8 rows
-// 1024 bytes apart.  The tile base must be 1024-byte aligned; stepping K by
+// `group` bytes apart (a multiple of 1024).  The tile base must be 1024-byte aligned; stepping K by
 // 16 elements inside the 128-byte row adds 32 bytes to the start address.
-__device__ __forceinline__ uint64_t sw128_kmajor_desc(uint32_t saddr)
+__device__ __forceinline__ uint64_t sw128_kmajor_desc(uint32_t saddr, uint32_t group = 1024)
 {
     return static_cast<uint64_t>((saddr >> 4) & 0x3FFFu)   // start address
            | (static_cast<uint64_t>(1) << 16)              // leading offset (unused here)
-           | (static_cast<uint64_t>(1024 >> 4) << 32)      // stride: 8 rows x 128 B
+           | (static_cast<uint64_t>(group >> 4) << 32)     // stride between groups of 8 rows
            | (static_cast<uint64_t>(1) << 46)              // descriptor version (sm_100)
            | (static_cast<uint64_t>(2) << 61);             // 128-byte swizzle
 }
@@ -398,6 +398,19 @@ __device__ __forceinline__ void tma_load_3d_pair(void *dst, const CUtensorMap *m
         "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
         ".L2::cache_hint [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(smem_addr(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(c0), "r"(c1), "r"(c2),
+        "l"(policy)
+        : "memory");
+}
+
+// 4-D form of tma_load_2d_pair (c0 innermost).
+__device__ __forceinline__ void tma_load_4d_pair(void *dst, const CUtensorMap *map,
+                                                 uint32_t bar_cluster, int32_t c0, int32_t c1,
+                                                 int32_t c2, int32_t c3, uint64_t policy)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        ".L2::cache_hint [%0], [%1, {%3, %4, %5, %6}], [%2], %7;" ::"r"(smem_addr(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(c0), "r"(c1), "r"(c2), "r"(c3),
         "l"(policy)
         : "memory");
 }

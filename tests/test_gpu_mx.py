@@ -163,6 +163,7 @@ SIZES = [
     ([1], 128, 8), ([3], 256, 136), ([2, 0, 1], 128, 1000), ([0, 5, 0, 0], 384, 264),
     ([37, 0, 128, 1, 200, 64], 640, 392), ([191, 193, 192], 512, 520), ([700, 16], 1408, 264),
     ([1] * 40, 256, 256), ([2, 1], 14336, 512), ([17] * 9, 2048, 640),
+    ([5, 4], 640, 72), ([4, 3], 384, 24), ([20], 1152, 40), ([3] * 5, 896, 264), ([7, 9, 1], 1536, 520),
     ([1], 4096, 256), ([0, 3], 3584, 8), ([1] * 75, 3200, 256),   # cut units of fewer chunks than there are CTA pairs
 ]
 
