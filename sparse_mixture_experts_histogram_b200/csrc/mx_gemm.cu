@@ -853,6 +853,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t buf = i % SM::kAccs;
             if (!bounded_wait_warp(&tfull[buf], (i / SM::kAccs) & 1u, abort_flag, p.err, kErrTimeoutMma)) break;
             ptx::tc_fence_after();
+            // The two warps of a quarter swap roles from unit to unit, so that
+            // units of one chunk keep both busy.
+            const int turn = half ^ static_cast<int>(i & 1u);
             const uint32_t tb = tmem + lane_base + buf * NMAX;
             const int nch = w.n / kColChunk;
             // output column of this lane: product, or h of the lane's quarter
@@ -861,7 +864,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const size_t pstep = static_cast<size_t>(p.part_cols) * 128;  // one CTA's part
             if (w.part >= 0) {
                 float *dst = p.parts + (static_cast<size_t>(w.part) * 2 + cta) * pstep + 32 * q + lane;
-                for (int c = half; c < nch; c += 2) {
+                for (int c = turn; c < nch; c += 2) {
                     uint32_t r[16];
                     ptx::tmem_ld16(tb + static_cast<uint32_t>(c * kColChunk), r);
                     ptx::tc_wait_ld();
@@ -870,7 +873,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         __stcg(dst + static_cast<size_t>(c * kColChunk + j) * 128, __uint_as_float(r[j]));
                 }
             } else {
-                for (int c = half; c < nch; c += 2) {
+                for (int c = turn; c < nch; c += 2) {
                     uint32_t r[16];
                     ptx::tmem_ld16(tb + static_cast<uint32_t>(c * kColChunk), r);
                     ptx::tc_wait_ld();
@@ -926,14 +929,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 uint32_t seen = 0;
                 uint32_t *ctr = p.ctr + (static_cast<size_t>(w.cut) * 2 + cta) * kEpiWarps +
-                                (GATED ? wpair : warp - 8);
+                                (GATED ? (q & 1) + 2 * turn : q + 4 * turn);
                 if (lane == 0) seen = atomicAdd(ctr, 1u);
                 seen = __shfl_sync(0xffffffffu, seen, 0);
                 const uint32_t all = static_cast<uint32_t>(w.last - w.first + 1) * (GATED ? 2u : 1u);
                 if (seen + 1 == all) {
                     __threadfence();
                     const float *base = p.parts + cta * pstep + lane + 32 * (GATED ? (q & 1) : q);
-                    for (int c = half; c < nch; c += 2) {
+                    for (int c = turn; c < nch; c += 2) {
                         for (int h8 = 0; h8 < 16 && c * kColChunk + h8 < w.hi; h8 += 8) {
                             float v[8], u[8];
 #pragma unroll
