@@ -796,8 +796,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int i = 0; i < 4; ++i) a[i] = src[32 * i + lane];
 #pragma unroll
                 for (int i = 0; i < kB; ++i) b[i] = src[128 + 32 * i + lane];
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(&cempty[slot]);
+                const uint32_t used = slot;
                 if (++slot == SM::kScSlots) {
                     slot = 0;
                     cphase ^= 1u;
@@ -827,6 +826,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::tc_wait_st();
                     ptx::tc_fence_before();
                     __syncwarp();
+                    // The slot is free only now that the loads' results have
+                    // been used: an arrival does not wait for the loads before
+                    // it, and the next copy then overtook them (seen as rare
+                    // wrong scales in one lane quarter).
+                    if (h == 0 && lane == 0) ptx::mbar_arrive(&cempty[used]);
                     if (lane == 0) ptx::mbar_arrive_pair(sfull0 + 8 * sb);
                     if (++sb == static_cast<uint32_t>(SM::kScBufs)) {
                         sb = 0;

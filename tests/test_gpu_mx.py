@@ -280,6 +280,35 @@ def test_gated_matches_formula(fmt, act, sizes, d, f):
     assert (np.abs(v - ref) <= tol + half).all()
 
 
+@pytest.mark.parametrize("fmt", [mx.E4M3, mx.E2M1])
+@pytest.mark.parametrize("sizes,d,f", [([700, 321, 1000], 2048, 4096), ([40, 61, 8, 77], 4096, 2048), ([3, 0, 9, 1], 4096, 4096)])
+def test_products_give_the_same_bits_every_time(fmt, sizes, d, f):
+    """Forty calls, other work between them: the pipelines hand over their
+    buffers in time whatever the timing."""
+    g = torch.Generator(device=DEV).manual_seed(7)
+    E, S = len(sizes), sum(sizes)
+
+    def codes(*shape, pitch):
+        q = torch.randint(0, 255 if fmt == mx.E2M1 or len(shape) == 3 else 0x77, shape, generator=g, device=DEV, dtype=torch.uint8)
+        return q, torch.randint(120, 130, (*shape[:-1], pitch), generator=g, device=DEV, dtype=torch.uint8)
+
+    x, xs = codes(S, d if fmt == mx.E4M3 else d // 2, pitch=mx.pitch(d))
+    W1, s1 = codes(E, f, d // 2, pitch=mx.pitch(d))
+    W3, s3 = codes(E, f, d // 2, pitch=mx.pitch(d))
+    off, ws = segments(sizes), ws_for(S, E, f)
+    h, y = torch.empty(S, f, dtype=torch.bfloat16, device=DEV), torch.empty(S, f, device=DEV)
+    first = None
+    for i in range(40):
+        moe.moe_mx_gated(S, d, E, f, fmt, x, xs, off, W1, s1, W3, s3, 1, h, None, None, ws)
+        moe.moe_mx_product(S, d, E, f, fmt, x, xs, off, W3, s3, 2, y, ws)
+        got = h.view(torch.int16).clone(), y.view(torch.int32).clone()
+        first = first or got
+        assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1]), i
+        if i % 3 == 0:
+            torch.randn(1 << (16 + i % 8), device=DEV)
+    ok(ws)
+
+
 def test_products_pass_nan_scales_on():
     rng = np.random.default_rng(1)
     S, K, N = 9, 256, 136
