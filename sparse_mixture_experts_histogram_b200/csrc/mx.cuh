@@ -32,17 +32,29 @@ __host__ __device__ constexpr int mx_scale_pitch(int cols)
     return (cols / kMxBlock + 15) & ~15;
 }
 
-// Scale byte for a block whose largest magnitude has the bits `amax` (a NaN
-// or an infinity among the values makes the exponent field 255).  amax =
-// m 2^(e - 127), 1 <= m < 2; the largest code is 1.75 * 2^8 or 1.5 * 2^2.
+// Scale byte for a block whose largest magnitude, finite, has the bits
+// `amax` = m 2^(e - 127), 1 <= m < 2: the largest code is 1.75 * 2^8 or
+// 1.5 * 2^2, so the byte is e - 8 (e - 2), one more when m is above 1.75 (1.5),
+// which the addition carries into the exponent.
+template <int FMT>
+__device__ __forceinline__ uint32_t mx_scale_code_finite(uint32_t amax)
+{
+    const int c = static_cast<int>((amax + (FMT == kMxE4M3 ? 0x1fffffu : 0x3fffffu)) >> 23) -
+                  (FMT == kMxE4M3 ? 8 : 2);
+    return static_cast<uint32_t>(max(c, 0));
+}
+
+// The same for any block: 255 when it holds a NaN or an infinity.
 template <int FMT>
 __device__ __forceinline__ uint32_t mx_scale_code(uint32_t amax)
 {
-    const int e = static_cast<int>(amax >> 23);
-    if (e == 255) return 255u;
-    const int up = (amax & 0x7fffffu) > (FMT == kMxE4M3 ? 0x600000u : 0x400000u);
-    const int c = e - (FMT == kMxE4M3 ? 8 : 2) + up;
-    return c < 0 ? 0u : static_cast<uint32_t>(c);
+    return amax >= 0x7f800000u ? 255u : mx_scale_code_finite<FMT>(amax);
+}
+
+// Two e4m3 codes, `lo` in the low byte, rounded to nearest even.
+__device__ __forceinline__ uint32_t e4m3x2(float lo, float hi)
+{
+    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
 }
 
 // 2^(127 - c), exact for every c that mx_scale_code gives; 0 for c = 255,
@@ -73,9 +85,7 @@ __device__ __forceinline__ uint2 mx_codes8(const float (&v)[8], uint32_t code)
         for (int i = 0; i < 4; ++i) {
             const float2 p = make_float2(v[2 * i] * inv, v[2 * i + 1] * inv);
             if constexpr (FMT == kMxE4M3)
-                w[i >> 1] |= static_cast<uint32_t>(
-                                 __nv_cvt_float2_to_fp8x2(p, __NV_SATFINITE, __NV_E4M3))
-                             << (16 * (i & 1));
+                w[i >> 1] |= e4m3x2(p.x, p.y) << (16 * (i & 1));
             else
                 w[0] |= static_cast<uint32_t>(
                             __nv_cvt_float2_to_fp4x2(p, __NV_E2M1, cudaRoundNearest))

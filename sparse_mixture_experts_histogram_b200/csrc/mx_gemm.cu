@@ -357,15 +357,31 @@ __device__ __forceinline__ void store_h8(const GemmParams &p, const float (&v)[8
         }
         return;
     }
-    uint32_t mine = 0;       // the scale byte of token t0 + lane
-    uint32_t w[2] = {0u, 0u};  // this lane's codes of tokens 0..3 and 4..7
+    uint32_t amax[8], worst = 0;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const uint32_t c = mx_scale_code<kMxE4M3>(__reduce_max_sync(0xffffffffu, abs_bits(v[j])));
+        amax[j] = __reduce_max_sync(0xffffffffu, abs_bits(v[j]));
+        worst = max(worst, amax[j]);
+    }
+    uint32_t mine = 0;         // the scale byte of token t0 + lane
+    float t[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const uint32_t c = mx_scale_code_finite<kMxE4M3>(amax[j]);
         if (lane == j) mine = c;
-        const uint32_t code =
-            c == 255u ? 0u : __nv_cvt_float_to_fp8(v[j] * mx_inv_scale(c), __NV_SATFINITE, __NV_E4M3);
-        w[j >> 2] |= code << (8 * (j & 3));
+        t[j] = v[j] * mx_inv_scale(c);
+    }
+    uint32_t w[2];             // this lane's codes of tokens 0..3 and 4..7
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+        w[g] = e4m3x2(t[4 * g], t[4 * g + 1]) | e4m3x2(t[4 * g + 2], t[4 * g + 3]) << 16;
+    if (worst >= 0x7f800000u) {  // a token with a NaN or an infinity: codes 0, scale 255
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+            if (amax[j] >= 0x7f800000u) {
+                if (lane == j) mine = 255u;
+                w[j >> 2] &= ~(0xffu << (8 * (j & 3)));
+            }
     }
     if (lane < 8 && t0 + lane >= lo && t0 + lane < hi) {
         uint8_t *s = p.qs + static_cast<size_t>(row + t0 + lane) * p.qpitch;
@@ -382,9 +398,9 @@ __device__ __forceinline__ void store_h8(const GemmParams &p, const float (&v)[8
         a = (lane & 1) ? __byte_perm(a, b, 0x3715) : __byte_perm(a, b, 0x6240);
         b = __shfl_xor_sync(0xffffffffu, a, 2);
         a = (lane & 2) ? __byte_perm(a, b, 0x3276) : __byte_perm(a, b, 0x5410);
-        const int t = t0 + 4 * g + (lane & 3);
-        if (t >= lo && t < hi)
-            *reinterpret_cast<uint32_t *>(p.q + static_cast<size_t>(row + t) * p.N + (f & ~3)) = a;
+        const int tok = t0 + 4 * g + (lane & 3);
+        if (tok >= lo && tok < hi)
+            *reinterpret_cast<uint32_t *>(p.q + static_cast<size_t>(row + tok) * p.N + (f & ~3)) = a;
     }
 }
 
@@ -884,11 +900,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if constexpr (GATED) {
                         // a warps keep tokens 0..7 of the chunk and hand 8..15
                         // to their b partner; b warps the other way round.
-                        float *mine = xa + xb * (2 * 8 * 32) + (is_a ? 0 : 8 * 32);
-                        float *theirs = xa + xb * (2 * 8 * 32) + (is_a ? 8 * 32 : 0);
+                        float *mine = xa + xb * (2 * 8 * 32) + (is_a ? 0 : 8 * 32) + lane;
+                        const float *theirs = xa + xb * (2 * 8 * 32) + (is_a ? 8 * 32 : 0) + lane;
+                        if (is_a) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            mine[j * 32 + lane] = __uint_as_float(r[is_a ? 8 + j : j]);
+                            for (int j = 0; j < 8; ++j) mine[j * 32] = __uint_as_float(r[8 + j]);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) mine[j * 32] = __uint_as_float(r[j]);
+                        }
                         ptx::mbar_arrive(&xbar[wpair * 2 + xb]);
                         const bool okx = bounded_wait(&xbar[wpair * 2 + xb], xuse[xb] & 1u, abort_flag,
                                                       p.err, kErrTimeoutEpi);
@@ -898,12 +918,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                             break;
                         }
                         float v[8];
+                        if (is_a) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const float ot = theirs[j * 32 + lane];
-                            const float g = is_a ? __uint_as_float(r[j]) : ot;
-                            const float b = is_a ? ot : __uint_as_float(r[8 + j]);
-                            v[j] = gate_mul(g, b, p.act);
+                            for (int j = 0; j < 8; ++j)
+                                v[j] = gate_mul(__uint_as_float(r[j]), theirs[j * 32], p.act);
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                v[j] = gate_mul(theirs[j * 32], __uint_as_float(r[8 + j]), p.act);
                         }
                         store_h8(p, v, w.r0, c * kColChunk + (is_a ? 0 : 8), w.lo, w.hi, o, lane);
                         xb ^= 1;
