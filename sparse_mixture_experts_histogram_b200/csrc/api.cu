@@ -239,22 +239,6 @@ cudaError_t make_tmap_rows(CUtensorMap *map, const void *base, uint64_t rows, ui
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t make_tmap_row_atoms(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols,
-                                uint64_t stride, uint32_t box_rows, uint32_t atoms)
-{
-    std::call_once(g_encode_once, load_encode);
-    if (g_encode == nullptr) return cudaErrorNotSupported;
-    const cuuint64_t dims[3] = {128, rows, cols / 128};
-    const cuuint64_t strides[2] = {stride, 128};
-    const cuuint32_t box[3] = {128, box_rows, atoms};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void *>(base),
-                                dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 cudaError_t make_tmap_e2m1_wide(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols,
                                 uint32_t box_rows, uint32_t atoms)
 {

@@ -208,11 +208,6 @@ struct MxGemmLaunch {
 // box_bytes x box_rows, 128-byte swizzled when box_bytes is 128.
 cudaError_t make_tmap_rows(CUtensorMap *map, const void *base, uint64_t rows, uint64_t bytes,
                            uint64_t stride, uint32_t box_bytes, uint32_t box_rows);
-// Rows of `cols` bytes (a multiple of 128), `stride` bytes apart, as columns
-// ("atoms") of 128 bytes: boxes of `atoms` x box_rows x 128 bytes, 128-byte
-// swizzled; coordinates (0, row, atom).
-cudaError_t make_tmap_row_atoms(CUtensorMap *map, const void *base, uint64_t rows, uint64_t cols,
-                                uint64_t stride, uint32_t box_rows, uint32_t atoms);
 // Tensor map of packed e2m1 rows (cols a multiple of 128, rows of 8, base
 // 32-byte aligned) whose copies spread 16 codes over 16 bytes of shared
 // memory, as the mixed 8/6/4-bit MMA reads 4-bit operands: boxes of box_rows

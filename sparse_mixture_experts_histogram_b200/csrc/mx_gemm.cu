@@ -77,7 +77,7 @@ struct Shape {
     static constexpr uint32_t kBTile = NMAX / 2 * kRowBytes;
     static constexpr int kAtoms = NMAX == 192 ? 1 : 2;  // 128-byte columns per stage
     static constexpr uint32_t kStage = kAtoms * (kATile + kBTile);
-    static constexpr int kStages = NMAX == 192 ? 6 : NMAX == 96 ? 4 : 5;
+    static constexpr int kStages = NMAX == 192 ? 6 : 4;
     static constexpr uint32_t kScSlot = kScA + NMAX * 16;
     static constexpr int kScSlots = 4;  // scale chunks in shared memory
     // Tensor memory: kAccs accumulators of NMAX columns (four where they
@@ -96,11 +96,13 @@ struct Shape {
                                      kWorkSlots * kWorkInts * 4 + 2 * (kMaxE + 1) * sizeof(int32_t);
     static_assert(kBytes <= 227 * 1024, "shared memory");
     static_assert(kBTile % 1024 == 0, "swizzle atom");
-    // Rows per copy of x and of its scales.  A copy that reaches beyond the
-    // last row of x is slow (2 rows of 14336 e4m3 values in copies of 16: 30
-    // us a product, 24 us without), so few token rows come in small copies.
-    static constexpr int kXBox = NMAX == 32 ? 8 : NMAX / 2;
-    static constexpr int kXsBox = NMAX == 32 ? 16 : NMAX;
+    // Rows per copy of x and of its scales: a tile is copied in as many as
+    // its columns need.  Few token rows come in small copies, since rows that
+    // the MMA does not read take L2 bandwidth from the weights (16 experts of
+    // 4096 -> 4096, 8 rows each: 45 us in copies of 48, 40 us in copies of
+    // 16) and a copy that reaches beyond the last row of x is slow.
+    static constexpr int kXBox = NMAX == 192 ? 96 : 16;
+    static constexpr int kXsBox = NMAX == 192 ? 192 : 32;
 };
 
 struct GemmParams {
@@ -247,17 +249,18 @@ struct Walk {
 
 // How many of `units` units of `chunks` chunks are taken whole: all of them,
 // or the full turns of the pairs while the rest is cut evenly.  Cutting costs
-// storing, waiting for and summing the parts, about as much as kJoin chunks;
-// it is taken where it saves more than that.
-constexpr int kJoin = 3;
-
-__device__ __forceinline__ int plan(int units, int pairs, int chunks)
+// storing, waiting for and summing the parts: about 3 us for 16 columns, 10 us
+// for 64, 30 us for 176, where a chunk takes about 1 us; it is taken where it
+// saves more chunks than that.  Measured: two rows of 14336 -> 4096 (28 chunks
+// down to 13) 33.5 us whole, 23.9 us cut; 64 rows of 2048 -> 4096 (4 down to
+// 1) 11 us whole, 19 us cut.
+__device__ __forceinline__ int plan(int units, int pairs, int chunks, int n)
 {
     const int full = units / pairs * pairs;
     const int rest = units - full;
     if (rest == 0) return units;
     const int each = (rest * chunks + pairs - 1) / pairs;
-    return chunks - each > kJoin ? full : units;
+    return chunks - each > 2 + n / 8 ? full : units;
 }
 
 template <int NMAX>
@@ -421,9 +424,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     // 8 rows: [group][atom][8 rows].  e2m1 rows: [atom][rows], a copy each.
     constexpr uint32_t kAGroup = FMT == kMxE4M3 ? kAtoms * 1024 : 1024;
     constexpr uint32_t kAAtom = FMT == kMxE4M3 ? 1024 : kATile;
-    constexpr bool kXSmall = FMT == kMxE4M3 && SM::kXBox == 8;
-    constexpr uint32_t kBGroup = kXSmall ? kAtoms * 1024 : 1024;
-    constexpr uint32_t kBAtom = kXSmall ? 1024 : SM::kBTile;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                                 ~static_cast<uintptr_t>(1023));
@@ -549,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (warp == 2) {
         __syncwarp();
         const int units = s_pre[E];
-        walk.start(static_cast<int>(blockIdx.x >> 1), pairs, units, plan(units, pairs, chunks), chunks);
+        walk.start(static_cast<int>(blockIdx.x >> 1), pairs, units, plan(units, pairs, chunks, p.part_cols), chunks);
         if (lane == 0) {
             int unit = 0;
             more = walk.next(w, unit);
@@ -610,12 +610,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int arow = w.e * p.N + w.blk * p.rows_blk + static_cast<int>(cta) * (p.rows_blk / 2);
             const int half = w.n >> 1;
             const int brow = w.r0 + static_cast<int>(cta) * half;
-            // Copies of x per CTA and their bytes per atom; with fewer rows
-            // than a copy would hold, the odd CTA has none.
-            const bool few = p.xbox < SM::kXBox;
-            const int nx = NMAX == 32 ? (few ? 1 - static_cast<int>(cta) : half / SM::kXBox) : 1;
-            const uint32_t tx = 2 * kAtoms * (FMT == kMxE4M3 ? kATile / 2 : kATile) +
-                                kAtoms * kRowBytes * (few ? p.xbox : 2 * SM::kXBox * (NMAX == 32 ? half / SM::kXBox : 1));
+            // Copies of x per atom: in this CTA, and in both.  Fewer than 8
+            // rows in all lie in the even CTA's columns.
+            const bool few = p.xbox < 8;
+            const int nx = few ? 1 - static_cast<int>(cta) : (half + p.xbox - 1) / p.xbox;
+            const int nx2 = few ? 1 : 2 * nx;
+            const uint32_t tx = kAtoms * (2 * (FMT == kMxE4M3 ? kATile / 2 : kATile) + kRowBytes * p.xbox * nx2);
             const int a1 = min(w.c1 * 2 * kAtomsPerHalf, atoms);
             for (int a = w.c0 * 2 * kAtomsPerHalf; a < a1; a += kAtoms) {
                 if (!bounded_wait_warp(&empty[stage], phase ^ 1u, abort_flag, p.err, kErrTimeoutMma)) {
@@ -632,26 +632,19 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ptx::tma_load_4d_pair(sa, &tmW1, fb, 0, 0, a, arow >> 3, pol);
                         if (GATED)
                             ptx::tma_load_4d_pair(sa + kAtoms * kATile / 2, &tmW3, fb, 0, 0, a, arow >> 3, pol);
-                        // [copy][atom][rows]: 8 rows a copy are a swizzle group
-                        if (few) {
-                            for (int t = 0; t < nx * kAtoms; ++t)
-                                ptx::tma_load_3d_pair(sa + kAtoms * kATile + t * kBAtom, &tmX, fb, 0, brow, a + t, pol);
-                        } else {
-                            for (int x = 0; x < nx; ++x)
-                                ptx::tma_load_3d_pair(sa + kAtoms * (kATile + x * SM::kXBox * kRowBytes), &tmX, fb, 0,
-                                                      brow + x * SM::kXBox, a, pol);
-                        }
                     } else {
 #pragma unroll
                         for (int t = 0; t < kAtoms; ++t) {
                             uint8_t *at = sa + t * kATile;
                             ptx::tma_load_2d_pair(at, &tmW1, fb, (a + t) * 128, arow, pol);
                             if (GATED) ptx::tma_load_2d_pair(at + kATile / 2, &tmW3, fb, (a + t) * 128, arow, pol);
-                            for (int x = 0; x < nx; ++x)
-                                ptx::tma_load_2d_pair(sa + kAtoms * kATile + t * SM::kBTile + x * SM::kXBox * kRowBytes,
-                                                      &tmX, fb, (a + t) * 128, brow + x * SM::kXBox, pol);
                         }
                     }
+#pragma unroll
+                    for (int t = 0; t < kAtoms; ++t)
+                        for (int x = 0; x < nx; ++x)
+                            ptx::tma_load_2d_pair(sa + kAtoms * kATile + t * SM::kBTile + x * p.xbox * kRowBytes,
+                                                  &tmX, fb, (a + t) * 128, brow + x * p.xbox, pol);
                 }
                 issued |= 1u << stage;
                 last_parity = (last_parity & ~(1u << stage)) | phase << stage;
@@ -708,7 +701,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             uint32_t stage = 0, phase = 0, sb = 0, sphase = 0;
             // Descriptors differ in their start address (16-byte units) only.
             const uint64_t desc_a = ptx::sw128_kmajor_desc(0, kAGroup);
-            const uint64_t desc_b = ptx::sw128_kmajor_desc(0, kBGroup);
+            const uint64_t desc_b = ptx::sw128_kmajor_desc(0);
             const uint32_t smem16 = ptx::smem_addr(smem) >> 4;
             const uint32_t fmt_a = FMT == kMxE4M3 ? ptx::kMxf8f6f4E2M1 : ptx::kMxf4E2M1;
             const uint32_t fmt_b = FMT == kMxE4M3 ? ptx::kMxf8f6f4E4M3 : ptx::kMxf4E2M1;
@@ -741,7 +734,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ptx::tc_fence_after();
                         const uint32_t a16 = smem16 + stage * (SM::kStage >> 4);
                         const uint64_t da = desc_a | (a16 + in_stage * (kAAtom >> 4));
-                        const uint64_t db = desc_b | (a16 + ((kAtoms * kATile + in_stage * kBAtom) >> 4));
+                        const uint64_t db = desc_b | (a16 + ((kAtoms * kATile + in_stage * SM::kBTile) >> 4));
                         const bool last = ++in_stage == kAtoms || h * kAtomsPerHalf + j + 1 == atoms;
                         if (one) {
                             if constexpr (FMT == kMxE4M3) {
@@ -864,7 +857,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int wpair = (q & 1) + 2 * half;  // (a, b) warp pairs: quarters (0,2) and (1,3)
         const bool is_a = q < 2;               // lanes 0..63: W1 products (gated)
         // for the slots of other pairs' parts
-        walk.start(static_cast<int>(blockIdx.x >> 1), pairs, s_pre[E], plan(s_pre[E], pairs, chunks), chunks);
+        walk.start(static_cast<int>(blockIdx.x >> 1), pairs, s_pre[E], plan(s_pre[E], pairs, chunks, p.part_cols), chunks);
         float *xa = xchg + wpair * (2 * 2 * 8 * 32);
         uint32_t xuse[2] = {0u, 0u};
         int xb = 0;
@@ -1039,7 +1032,8 @@ int pair_count(cudaLaunchConfig_t &cfg)
     return n;
 }
 
-int part_cols(int S) { return std::min(kMaxN, (S + 15) / 16 * 16); }
+// Columns of the widest tile.
+int part_cols(int S, int nmax) { return std::min(nmax, (S + 15) / 16 * 16); }
 
 template <int FMT, bool GATED, int NMAX>
 cudaError_t launch_t(const MxGemmLaunch &a, cudaStream_t s)
@@ -1047,8 +1041,8 @@ cudaError_t launch_t(const MxGemmLaunch &a, cudaStream_t s)
     using SM = Shape<NMAX>;
     const uint64_t wrows = static_cast<uint64_t>(a.E) * a.N;
     const uint32_t abox = GATED ? 64 : 128;
-    const int xbox = NMAX == 32 ? std::min(SM::kXBox, a.S) : SM::kXBox;
-    const int xsbox = NMAX == 32 ? std::min(SM::kXsBox, a.S) : SM::kXsBox;
+    const int xbox = a.S < 8 ? a.S : a.S < SM::kXBox ? 8 : SM::kXBox;
+    const int xsbox = std::min(SM::kXsBox, a.S);
     const int nsc = a.K / kMxBlock, wsc = mx_scale_pitch(a.K);
     CUtensorMap tW1, tW3, tX, tS1, tS3, tXs;
     auto weights = [&](CUtensorMap *m, const uint8_t *w) {
@@ -1065,8 +1059,7 @@ cudaError_t launch_t(const MxGemmLaunch &a, cudaStream_t s)
         tS3 = tS1;
     }
     if (e == cudaSuccess)
-        e = FMT == kMxE4M3 ? make_tmap_row_atoms(&tX, a.x, a.S, a.K, a.x_stride, xbox, xbox < SM::kXBox ? 1 : SM::kAtoms)
-                           : make_tmap_rows(&tX, a.x, a.S, a.K / 2, a.x_stride, 128, xbox);
+        e = make_tmap_rows(&tX, a.x, a.S, FMT == kMxE4M3 ? a.K : a.K / 2, a.x_stride, 128, xbox);
     if (e == cudaSuccess) e = make_tmap_rows(&tXs, a.xs, a.S, nsc, a.xs_stride, 16, xsbox);
     if (e != cudaSuccess) return e;
     auto *kernel = mx_pair_kernel<FMT, GATED, NMAX>;
@@ -1087,7 +1080,7 @@ cudaError_t launch_t(const MxGemmLaunch &a, cudaStream_t s)
     p.qpitch = mx_scale_pitch(a.N);
     p.ctr = reinterpret_cast<uint32_t *>(a.counters);
     p.parts = reinterpret_cast<float *>(a.scratch);
-    p.part_cols = part_cols(a.S);
+    p.part_cols = part_cols(a.S, NMAX);
     p.err = a.err;
 
     cudaLaunchConfig_t cfg = {};
@@ -1114,9 +1107,11 @@ cudaError_t launch_t(const MxGemmLaunch &a, cudaStream_t s)
 template <int FMT, bool GATED>
 cudaError_t launch_n(const MxGemmLaunch &a, cudaStream_t s)
 {
-    const int rows = (a.S + a.E - 1) / a.E;  // per expert, when they are even
-    if (rows <= 24) return launch_t<FMT, GATED, 32>(a, s);
-    if (rows <= 72) return launch_t<FMT, GATED, 96>(a, s);
+    // Rows per expert if they were even.  16 experts of 4096 -> 4096 with
+    // uneven segments, e4m3 rows, tiles of at most 96 / 192 rows: 8 rows an
+    // expert 40 / 47 us, 32: 41 / 45, 64: 42 / 44, 80: 50 / 45, 96: 55 / 45.
+    const int rows = (a.S + a.E - 1) / a.E;
+    if (rows <= 64) return launch_t<FMT, GATED, 96>(a, s);
     return launch_t<FMT, GATED, 192>(a, s);
 }
 
@@ -1141,7 +1136,7 @@ size_t mx_gemm_zero_bytes() { return kCounters * sizeof(uint32_t); }
 
 size_t mx_gemm_scratch_bytes(int S)
 {
-    return static_cast<size_t>(kParts) * 2 * 128 * part_cols(S) * sizeof(float);
+    return static_cast<size_t>(kParts) * 2 * 128 * part_cols(S, kMaxN) * sizeof(float);
 }
 
 cudaError_t launch_mx_gemm(const MxGemmLaunch &a, cudaStream_t s)
