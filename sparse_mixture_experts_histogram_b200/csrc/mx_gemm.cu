@@ -60,7 +60,6 @@ constexpr uint32_t kRowBytes = 128;      // of an operand row in shared memory
 constexpr uint32_t kATile = 128 * kRowBytes;
 constexpr int kChunkK = 512;             // values of K per scale chunk (16 scale bytes)
 constexpr uint32_t kScA = 128 * 16;      // bytes of a chunk's weight scales
-constexpr int kHalfK = 256;              // values of K per scale buffer in tensor memory
 constexpr int kWorkSlots = 4;            // units announced ahead by the scheduling warp
 constexpr int kWorkInts = 16;
 constexpr uint32_t kTmemCols = 512;
@@ -70,25 +69,35 @@ constexpr int kMaxPairs = 80;            // pairs a launch may use (74 on 148 SM
 constexpr int kParts = 2 * kMaxPairs;    // partial units: two per pair
 constexpr size_t kCounters = static_cast<size_t>(kMaxPairs) * 2 * kEpiWarps;
 
-// Layout by the largest token tile: fewer token rows leave room for more
-// stages, which a weight stream needs in flight.
-template <int NMAX>
+// Layout by the format of x and the largest token tile.  A stage is one step
+// of the MMA warp: kAtoms 128-byte columns of both operands, whose MMAs it
+// issues in one straight run behind one wait.  (Waits and branches between
+// fewer MMAs cost more than the MMAs of a narrow tile: 2000 rows over 256
+// experts of 2048 -> 7168, e4m3, 4 MMAs a run 414 us, 8 a run 344 us.)
+template <int FMT, int NMAX>
 struct Shape {
+    static constexpr int kAtoms = 2;
+    static constexpr int kAtomK = FMT == kMxE4M3 ? 128 : 256;  // values of K per column
+    static constexpr int kStepK = kAtoms * kAtomK;
+    static constexpr int kSteps = kChunkK / kStepK;            // per chunk
+    static constexpr int kMmas = 4 * kAtoms;                   // per step
+    static constexpr int kMmaK = kAtomK / 4;
     static constexpr uint32_t kBTile = NMAX / 2 * kRowBytes;
-    static constexpr int kAtoms = NMAX == 192 ? 1 : 2;  // 128-byte columns per stage
     static constexpr uint32_t kStage = kAtoms * (kATile + kBTile);
-    static constexpr int kStages = NMAX == 192 ? 6 : 4;
+    static constexpr int kStages = (NMAX == 192 ? 6 : 8) / kAtoms;
     static constexpr uint32_t kScSlot = kScA + NMAX * 16;
     static constexpr int kScSlots = 4;  // scale chunks in shared memory
     // Tensor memory: kAccs accumulators of NMAX columns (four where they
     // fit: short units then overlap the latency of several epilogues), then
-    // kScBufs buffers of the scales of 256 values of K.  128 values are one
-    // 32-bit word a row: 4 columns of A's scales, then NMAX / 32 of B's.
+    // kScBufs buffers of the scales of a step.  128 values of K are one 32-bit
+    // word a row: 4 columns of A's scales, then NMAX / 32 of B's.
     static constexpr int kAccs = NMAX == 192 ? 2 : 4;
     static constexpr uint32_t kWord = NMAX == 192 ? 12 : 8;
+    static constexpr int kWords = kStepK / 128;
+    static constexpr uint32_t kScBuf = kWords * kWord;
     static constexpr uint32_t kScCol = kAccs * NMAX;
-    static constexpr int kScBufs = NMAX == 192 ? 5 : 8;
-    static_assert(kScCol + kScBufs * 2 * kWord <= kTmemCols, "tensor memory");
+    static constexpr int kScBufs = (kTmemCols - kScCol) / kScBuf;
+    static_assert(kScBufs >= 2, "tensor memory");
     static constexpr int kBarriers = 2 * kStages + 2 * kScSlots + 2 * kAccs + 2 * kScBufs +
                                      2 * kWorkSlots + 1 + 8;
     static constexpr size_t kBytes = 1024 /* alignment slack */ + kStages * kStage +
@@ -415,11 +424,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                    const __grid_constant__ CUtensorMap tmS3, const __grid_constant__ CUtensorMap tmXs,
                    const GemmParams p)
 {
-    using SM = Shape<NMAX>;
+    using SM = Shape<FMT, NMAX>;
     constexpr int kStages = SM::kStages;
     constexpr int kAtoms = SM::kAtoms;
-    constexpr int kAtomK = FMT == kMxE4M3 ? 128 : 256;  // values of K per atom
-    constexpr int kAtomsPerHalf = kHalfK / kAtomK;
     // e4m3 rows: one copy spreads the weights of a stage's atoms, in groups of
     // 8 rows: [group][atom][8 rows].  e2m1 rows: [atom][rows], a copy each.
     constexpr uint32_t kAGroup = FMT == kMxE4M3 ? kAtoms * 1024 : 1024;
@@ -460,8 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int E = p.offsets ? p.E : 1;
     const int blocks = (p.N + p.rows_blk - 1) / p.rows_blk;
     const int chunks = (p.K + kChunkK - 1) / kChunkK;
-    const int atoms = (p.K + kAtomK - 1) / kAtomK;
-    const int halves = (p.K + kHalfK - 1) / kHalfK;
+    const int steps = (p.K + SM::kStepK - 1) / SM::kStepK;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
@@ -616,8 +622,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int nx = few ? 1 - static_cast<int>(cta) : (half + p.xbox - 1) / p.xbox;
             const int nx2 = few ? 1 : 2 * nx;
             const uint32_t tx = kAtoms * (2 * (FMT == kMxE4M3 ? kATile / 2 : kATile) + kRowBytes * p.xbox * nx2);
-            const int a1 = min(w.c1 * 2 * kAtomsPerHalf, atoms);
-            for (int a = w.c0 * 2 * kAtomsPerHalf; a < a1; a += kAtoms) {
+            const int s1 = min(w.c1 * SM::kSteps, steps);
+            for (int st = w.c0 * SM::kSteps; st < s1; ++st) {
+                const int a = st * kAtoms;
                 if (!bounded_wait_warp(&empty[stage], phase ^ 1u, abort_flag, p.err, kErrTimeoutMma)) {
                     stop = true;
                     break;
@@ -705,7 +712,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint32_t smem16 = ptx::smem_addr(smem) >> 4;
             const uint32_t fmt_a = FMT == kMxE4M3 ? ptx::kMxf8f6f4E2M1 : ptx::kMxf4E2M1;
             const uint32_t fmt_b = FMT == kMxE4M3 ? ptx::kMxf8f6f4E4M3 : ptx::kMxf4E2M1;
-            const bool odd_end = p.K % kHalfK != 0;   // the last 256 values of K are only 128
             bool stop = false;
             for (uint32_t i = 0; !stop && next_unit(); ++i) {
                 const uint32_t buf = i % SM::kAccs;
@@ -715,64 +721,52 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ptx::tc_fence_after();
                 const uint32_t dacc = tmem + buf * NMAX;
                 uint32_t acc = 0;
-                int in_stage = 0;  // atoms of the stage used so far
-                const int h1 = min(2 * w.c1, halves);
-                for (int h = 2 * w.c0; h < h1 && !stop; ++h) {
-                    if (!bounded_wait_warp(&sfull[sb], sphase, abort_flag, p.err, kErrTimeoutTma)) {
+                // One MMA of a step: column t = m / 4 of the operands, 32 bytes
+                // of its rows.  e4m3 rows: 32 values, byte kk of the column's
+                // word of scales.  e2m1 rows: 64 values, two bytes of the
+                // first or second of the column's two words.
+                auto mma = [&](int m, uint32_t a16, uint32_t word0, uint32_t accumulate) {
+                    const int t = m >> 2, kk = m & 3;
+                    const uint64_t da = desc_a | (a16 + t * (kAAtom >> 4));
+                    const uint64_t db = desc_b | (a16 + ((kAtoms * kATile + t * SM::kBTile) >> 4));
+                    if constexpr (FMT == kMxE4M3) {
+                        const uint32_t word = word0 + SM::kWord * t;
+                        ptx::tc_mma_mxf8f6f4_pair(dacc, da + 2 * kk, db + 2 * kk, idesc + ptx::idesc_mx_sf(kk),
+                                                  word, word + 4, accumulate);
+                    } else {
+                        const uint32_t word = word0 + SM::kWord * (2 * t + (kk >> 1));
+                        ptx::tc_mma_mxf4_pair(dacc, da + 2 * kk, db + 2 * kk,
+                                              idesc + ptx::idesc_mx_sf(2 * (kk & 1)), word, word + 4, accumulate);
+                    }
+                };
+                const int s1 = min(w.c1 * SM::kSteps, steps);
+                for (int st = w.c0 * SM::kSteps; st < s1; ++st) {
+                    if (!bounded_wait_warp(&sfull[sb], sphase, abort_flag, p.err, kErrTimeoutTma) ||
+                        !bounded_wait_warp(&full[stage], phase, abort_flag, p.err, kErrTimeoutTma)) {
                         stop = true;
                         break;
                     }
-                    const uint32_t word0 = tmem + SM::kScCol + sb * (2 * SM::kWord);
+                    ptx::tc_fence_after();
+                    const uint32_t a16 = smem16 + stage * (SM::kStage >> 4);
+                    const uint32_t word0 = tmem + SM::kScCol + sb * SM::kScBuf;
+                    const int left = (p.K - st * SM::kStepK) / SM::kMmaK;  // MMAs up to the end of K
+                    if (one) {
+                        if (left >= SM::kMmas) {
 #pragma unroll
-                    for (int j = 0; j < kAtomsPerHalf; ++j) {
-                        if (h * kAtomsPerHalf + j >= atoms) break;
-                        if (in_stage == 0 &&
-                            !bounded_wait_warp(&full[stage], phase, abort_flag, p.err, kErrTimeoutTma)) {
-                            stop = true;
-                            break;
+                            for (int m = 0; m < SM::kMmas; ++m) mma(m, a16, word0, m ? 1u : acc);
+                        } else {
+#pragma unroll
+                            for (int m = 0; m < SM::kMmas; ++m)
+                                if (m < left) mma(m, a16, word0, m ? 1u : acc);
                         }
-                        ptx::tc_fence_after();
-                        const uint32_t a16 = smem16 + stage * (SM::kStage >> 4);
-                        const uint64_t da = desc_a | (a16 + in_stage * (kAAtom >> 4));
-                        const uint64_t db = desc_b | (a16 + ((kAtoms * kATile + in_stage * SM::kBTile) >> 4));
-                        const bool last = ++in_stage == kAtoms || h * kAtomsPerHalf + j + 1 == atoms;
-                        if (one) {
-                            if constexpr (FMT == kMxE4M3) {
-                                // 4 x 32 values, bytes 0..3 of one word
-                                const uint32_t word = word0 + SM::kWord * j;
-#pragma unroll
-                                for (int kk = 0; kk < 4; ++kk)
-                                    ptx::tc_mma_mxf8f6f4_pair(dacc, da + 2 * kk, db + 2 * kk,
-                                                              idesc + ptx::idesc_mx_sf(kk), word, word + 4,
-                                                              kk ? 1u : acc);
-                            } else {
-                                // 4 x 64 values, two bytes each of two words
-#pragma unroll
-                                for (int kk = 0; kk < 2; ++kk)
-                                    ptx::tc_mma_mxf4_pair(dacc, da + 2 * kk, db + 2 * kk,
-                                                          idesc + ptx::idesc_mx_sf(2 * kk), word0, word0 + 4,
-                                                          kk ? 1u : acc);
-                                if (!odd_end || h + 1 < halves) {
-#pragma unroll
-                                    for (int kk = 2; kk < 4; ++kk)
-                                        ptx::tc_mma_mxf4_pair(dacc, da + 2 * kk, db + 2 * kk,
-                                                              idesc + ptx::idesc_mx_sf(2 * (kk - 2)),
-                                                              word0 + SM::kWord, word0 + SM::kWord + 4, 1u);
-                                }
-                            }
-                            if (last) ptx::tc_commit_pair(&empty[stage], 0x3);
-                        }
-                        acc = 1;
-                        if (last) {
-                            in_stage = 0;
-                            if (++stage == static_cast<uint32_t>(kStages)) {
-                                stage = 0;
-                                phase ^= 1u;
-                            }
-                        }
+                        ptx::tc_commit_pair(&empty[stage], 0x3);
+                        ptx::tc_commit_pair(&sempty[sb], 0x3);
                     }
-                    if (stop) break;
-                    if (one) ptx::tc_commit_pair(&sempty[sb], 0x3);
+                    acc = 1;
+                    if (++stage == static_cast<uint32_t>(kStages)) {
+                        stage = 0;
+                        phase ^= 1u;
+                    }
                     if (++sb == static_cast<uint32_t>(SM::kScBufs)) {
                         sb = 0;
                         sphase ^= 1u;
@@ -811,27 +805,29 @@ __global__ void __launch_bounds__(kThreads, 1)
                     cphase ^= 1u;
                 }
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (2 * c + h >= halves) break;
+                for (int h = 0; h < SM::kSteps; ++h) {
+                    if (SM::kSteps * c + h >= steps) break;
                     if (!bounded_wait_warp(&sempty[sb], sphase ^ 1u, abort_flag, p.err, kErrTimeoutMma)) {
                         stop = true;
                         break;
                     }
                     ptx::tc_fence_after();
-                    uint32_t r[2 * SM::kWord];
+                    uint32_t r[SM::kScBuf];
 #pragma unroll
-                    for (int j = 0; j < 2; ++j)
+                    for (int j = 0; j < SM::kWords; ++j)
 #pragma unroll
                         for (int i = 0; i < static_cast<int>(SM::kWord); ++i) {
                             uint32_t v = 0u;
-                            if (i < 4) v = reinterpret_cast<const uint32_t *>(&a[i])[2 * h + j];
-                            else if (i - 4 < kB) v = reinterpret_cast<const uint32_t *>(&b[i - 4])[2 * h + j];
+                            if (i < 4) v = reinterpret_cast<const uint32_t *>(&a[i])[SM::kWords * h + j];
+                            else if (i - 4 < kB) v = reinterpret_cast<const uint32_t *>(&b[i - 4])[SM::kWords * h + j];
                             r[SM::kWord * j + i] = v;
                         }
-                    const uint32_t dst = tq + sb * (2 * SM::kWord);
-                    ptx::tmem_st16(dst, *reinterpret_cast<const uint32_t(*)[16]>(&r[0]));
-                    if constexpr (SM::kWord == 12)
-                        ptx::tmem_st8(dst + 16, *reinterpret_cast<const uint32_t(*)[8]>(&r[16]));
+                    const uint32_t dst = tq + sb * SM::kScBuf;
+#pragma unroll
+                    for (int z = 0; z + 16 <= static_cast<int>(SM::kScBuf); z += 16)
+                        ptx::tmem_st16(dst + z, *reinterpret_cast<const uint32_t(*)[16]>(&r[z]));
+                    if constexpr (SM::kScBuf % 16 != 0)
+                        ptx::tmem_st8(dst + SM::kScBuf - 8, *reinterpret_cast<const uint32_t(*)[8]>(&r[SM::kScBuf - 8]));
                     ptx::tc_wait_st();
                     ptx::tc_fence_before();
                     __syncwarp();
@@ -1038,7 +1034,7 @@ int part_cols(int S, int nmax) { return std::min(nmax, (S + 15) / 16 * 16); }
 template <int FMT, bool GATED, int NMAX>
 cudaError_t launch_t(const MxGemmLaunch &a, cudaStream_t s)
 {
-    using SM = Shape<NMAX>;
+    using SM = Shape<FMT, NMAX>;
     const uint64_t wrows = static_cast<uint64_t>(a.E) * a.N;
     const uint32_t abox = GATED ? 64 : 128;
     const int xbox = a.S < 8 ? a.S : a.S < SM::kXBox ? 8 : SM::kXBox;
