@@ -1104,8 +1104,12 @@ static moe_status mx_gemm(MxGemmLaunch &a, void *ws, size_t ws_bytes, moe_stream
     a.err = reinterpret_cast<uint32_t *>(wsb);
     a.counters = wsb + kHeaderBytes;
     a.scratch = a.counters + align_up(mx_gemm_zero_bytes());
-    const moe_status st = from_cuda(launch_clear(wsb, kHeaderBytes + mx_gemm_zero_bytes(), s));
-    if (st != MOE_OK) return st;
+    if (mx_gemm_needs_counters(a)) {
+        const moe_status st = from_cuda(launch_clear(wsb, kHeaderBytes + mx_gemm_zero_bytes(), s));
+        if (st != MOE_OK) return st;
+    } else {
+        a.own_err = true;
+    }
     a.pdl = true;
     return from_cuda(launch_mx_gemm(a, s));
 }

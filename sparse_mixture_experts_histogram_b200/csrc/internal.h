@@ -198,9 +198,11 @@ struct MxGemmLaunch {
     int y_type;
     void *y;                  // [S, N] bf16 or fp32, or nullptr (gated, e4m3 out)
     uint8_t *q, *qs;          // [S, N] e4m3 and scale bytes [S, pitch(N)]
-    uint8_t *counters;        // mx_gemm_zero_bytes(), zero before the launch
+    uint8_t *counters;        // mx_gemm_zero_bytes(), zero before the launch where
+                              // mx_gemm_needs_counters()
     uint8_t *scratch;         // mx_gemm_scratch_bytes()
     uint32_t *err;
+    bool own_err;             // the launch resets *err itself
     bool pdl;
 };
 
@@ -218,6 +220,7 @@ cudaError_t make_tmap_e2m1_wide(CUtensorMap *map, const void *base, uint64_t row
 
 size_t mx_gemm_scratch_bytes(int S);
 size_t mx_gemm_zero_bytes();
+bool mx_gemm_needs_counters(const MxGemmLaunch &a);
 cudaError_t launch_rmsnorm(const NormLaunch &a, cudaStream_t s);
 cudaError_t launch_mx_quantize(const MxQuantLaunch &a, cudaStream_t s);
 cudaError_t launch_clear(void *p, size_t bytes, cudaStream_t s);  // 16-byte multiples

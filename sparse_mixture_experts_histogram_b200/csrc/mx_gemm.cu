@@ -15,15 +15,15 @@
 // product 128 output columns, of the gated form 64 rows of W1 and the same 64
 // of W3, so that both sums of an output lie in one CTA.
 //
-// Operands reach shared memory as 128-byte rows by TMA: 128 (e4m3) or 256
-// (e2m1) values of K a stage.  Against e4m3 rows the copy spreads 16 weight
-// codes over 16 bytes, the layout of the mixed kind, so HBM and L2 carry 4
-// bits a weight.  Scales are copied 16 to a row (512 values of K, a chunk);
-// four warps move them from shared to tensor memory in the MMA's layout (row
-// r in lane r % 32 of every lane quarter, column r / 32), two chunks deep.
-// The row-major scales of a checkpoint can be used as they are, and rows of x
-// can start at any row: no 128-row tiling of the scales has to fit the
-// segments.
+// Operands reach shared memory as 128-byte rows by TMA, two columns of 128
+// bytes a stage: 256 (e4m3) or 512 (e2m1) values of K.  Against e4m3 rows the
+// copy spreads 16 weight codes over 16 bytes, the layout of the mixed kind, so
+// HBM and L2 carry 4 bits a weight.  Scales are copied 16 to a row (512 values
+// of K, a chunk); four warps move them from shared to tensor memory in the
+// MMA's layout (row r in lane r % 32 of every lane quarter, column r / 32),
+// several stages ahead.  The row-major scales of a checkpoint can be used as
+// they are, and rows of x can start at any row: no 128-row tiling of the
+// scales has to fit the segments.
 //
 // Work: a unit is (expert, 256 weight rows, token tile).  Pairs take whole
 // units in turn; what does not fill the last turn is cut along K into equal
@@ -33,9 +33,18 @@
 // the result does not depend on who was last.
 //
 // Roles per CTA: warp 0 issues the copies, warp 1 of the even CTA the MMAs
-// (two accumulators), warps 4..7 move scales, warps 8..15 drain the
-// accumulator; warp 2 decodes units ahead for all of them and warp 3 copies
+// (two to four accumulators), warps 4..7 move scales, warps 8..15 drain the
+// accumulators; warp 2 decodes units ahead for all of them and warp 3 copies
 // scales.  All waits are bounded.
+//
+// What bounds it, at the rates of a plain copy (6.54 TB/s) and a bf16 library
+// product (1607 TFLOP/s) on the same card: few rows an expert, the weights'
+// bytes and, with e4m3 rows, the issue of MMAs (2000 rows over 256 experts of
+// 2048 -> 7168: 355 us, 5.7 TB/s; e2m1 rows 297 us, 6.8 TB/s); one token, the
+// latency of a launch's ends (14336 -> 4096, 2 experts: 22 us, of which 10 us are the
+// bytes); prefill, the operands' way from L2 through shared memory and the
+// power cap (8192 rows, 14336 -> 4096: 367 us, 2.6 PFLOP/s; e2m1 rows 198 us,
+// 4.9 PFLOP/s; gated 4096 -> 2 x 14336 with e4m3 out: 733 us, 2.6 PFLOP/s).
 //
 // Method: as gemm_pair.cu; the pages' deployment section (jsqmd.com) asks for
 // quantised experts.
@@ -127,6 +136,7 @@ struct GemmParams {
     int part_cols;
     uint32_t *ctr;           // kCounters, zero before the launch
     uint32_t *err;
+    int own_err;             // the error word is this launch's alone: it resets it
 };
 
 // ------------------------------------------------------------------ waiting
@@ -263,13 +273,15 @@ struct Walk {
 // saves more chunks than that.  Measured: two rows of 14336 -> 4096 (28 chunks
 // down to 13) 33.5 us whole, 23.9 us cut; 64 rows of 2048 -> 4096 (4 down to
 // 1) 11 us whole, 19 us cut.
+__host__ __device__ constexpr int join_chunks(int n) { return 2 + n / 8; }
+
 __device__ __forceinline__ int plan(int units, int pairs, int chunks, int n)
 {
     const int full = units / pairs * pairs;
     const int rest = units - full;
     if (rest == 0) return units;
     const int each = (rest * chunks + pairs - 1) / pairs;
-    return chunks - each > 2 + n / 8 ? full : units;
+    return chunks - each > join_chunks(n) ? full : units;
 }
 
 template <int NMAX>
@@ -532,9 +544,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         bad = __any_sync(0xffffffffu, bad);
-        if (bad) {
-            nu = 0;
-            if (lane == 0 && leader) atomicOr(p.err, kErrOffsets);
+        if (bad) nu = 0;
+        // Every pair sees the same table.  The other bits are set by waits
+        // that ran out, seconds after this store.
+        if (p.own_err) {
+            if (blockIdx.x == 0 && lane == 0) *p.err = bad ? kErrOffsets : 0u;
+        } else if (bad && lane == 0 && leader) {
+            atomicOr(p.err, kErrOffsets);
         }
         const int incl = warp_scan_incl(nu, lane);
         int run = incl - nu;
@@ -1078,6 +1094,7 @@ cudaError_t launch_t(const MxGemmLaunch &a, cudaStream_t s)
     p.parts = reinterpret_cast<float *>(a.scratch);
     p.part_cols = part_cols(a.S, NMAX);
     p.err = a.err;
+    p.own_err = a.own_err ? 1 : 0;
 
     cudaLaunchConfig_t cfg = {};
     cfg.blockDim = dim3(kThreads);
@@ -1100,15 +1117,21 @@ cudaError_t launch_t(const MxGemmLaunch &a, cudaStream_t s)
     return cudaLaunchKernelEx(&cfg, kernel, tW1, tW3, tX, tS1, tS3, tXs, p);
 }
 
-template <int FMT, bool GATED>
-cudaError_t launch_n(const MxGemmLaunch &a, cudaStream_t s)
+// Largest token tile of a launch.
+int tile_rows(const MxGemmLaunch &a)
 {
     // Rows per expert if they were even.  16 experts of 4096 -> 4096 with
     // uneven segments, e4m3 rows, tiles of at most 96 / 192 rows: 8 rows an
     // expert 40 / 47 us, 32: 41 / 45, 64: 42 / 44, 80: 50 / 45, 96: 55 / 45.
     const int rows = (a.S + a.E - 1) / a.E;
-    if (rows <= 64) return launch_t<FMT, GATED, 96>(a, s);
-    return launch_t<FMT, GATED, 192>(a, s);
+    return rows <= 64 ? 96 : kMaxN;
+}
+
+template <int FMT, bool GATED>
+cudaError_t launch_n(const MxGemmLaunch &a, cudaStream_t s)
+{
+    if (tile_rows(a) == 96) return launch_t<FMT, GATED, 96>(a, s);
+    return launch_t<FMT, GATED, kMaxN>(a, s);
 }
 
 }  // namespace
@@ -1133,6 +1156,13 @@ size_t mx_gemm_zero_bytes() { return kCounters * sizeof(uint32_t); }
 size_t mx_gemm_scratch_bytes(int S)
 {
     return static_cast<size_t>(kParts) * 2 * 128 * part_cols(S, kMaxN) * sizeof(float);
+}
+
+bool mx_gemm_needs_counters(const MxGemmLaunch &a)
+{
+    // plan() leaves every unit whole when even one chunk a pair saves too little
+    const int chunks = (a.K + kChunkK - 1) / kChunkK;
+    return chunks - 1 > join_chunks(part_cols(a.S, tile_rows(a)));
 }
 
 cudaError_t launch_mx_gemm(const MxGemmLaunch &a, cudaStream_t s)

@@ -364,6 +364,70 @@ def test_segments_may_start_behind_row_zero():
     assert (y[:4] == 7).all() and (y[21:] == 7).all()
 
 
+def test_empty_segments_write_nothing():
+    rng = np.random.default_rng(4)
+    S, K, N, E = 5, 256, 128, 4
+    x, W = mx.Matrix(rng, (S, K), mx.E4M3), mx.Matrix(rng, (E, N, K), mx.E2M1)
+    y, hq, hs = torch.full((S, N), 7.0, device=DEV), byte(S, N), byte(S, mx.pitch(N))
+    ws = ws_for(S, E, N)
+    for at in (0, 3, 5):
+        off = torch.full((E + 1,), at, dtype=torch.int32, device=DEV)
+        moe.moe_mx_product(S, K, E, N, mx.E4M3, x.q, x.s, off, W.q, W.s, 2, y, ws)
+        moe.moe_mx_gated(S, K, E, N, mx.E4M3, x.q, x.s, off, W.q, W.s, W.q, W.s, 0, None, hq, hs, ws)
+        ok(ws)
+    assert (y == 7).all() and (hq == 0xA5).all() and (hs == 0xA5).all()
+
+
+@pytest.mark.parametrize("fmt", [mx.E4M3, mx.E2M1])
+def test_many_experts_and_tile_borders(fmt):
+    """256 experts, segments at and around the tile sizes, weights that start
+    32 bytes into their allocation."""
+    rng = np.random.default_rng(6)
+    E, K, N = 256, 128, 16
+    sizes = np.zeros(E, np.int64)
+    sizes[[0, 3, 4, 77, 200, 254, 255]] = (192, 193, 1, 96, 97, 384, 16)
+    S = int(sizes.sum())
+    x, W = mx.Matrix(rng, (S, K), fmt), mx.Matrix(rng, (E, N, K), mx.E2M1)
+    room = torch.empty(W.q.numel() + 64, dtype=torch.uint8, device=DEV)
+    Wq = room[32:32 + W.q.numel()].view_as(W.q).copy_(W.q)
+    y, ws = torch.empty(S, N, device=DEV), ws_for(S, E, N)
+    moe.moe_mx_product(S, K, E, N, fmt, x.q, x.s, segments(sizes), Wq, W.s, 2, y, ws)
+    ok(ws)
+    ref, mag = product_ref(x.v, W.v, sizes)
+    assert (np.abs(f64(y) - ref) <= K * 2.0 ** -23 * mag).all()
+
+
+def test_indices_beyond_32_bits():
+    """More than 2^31 elements in, and more than 2^31 out: the last rows."""
+    rows, cols = 70000, 32768
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device=DEV).normal_(generator=torch.Generator(device=DEV).manual_seed(1))
+    q, s = torch.empty(rows, cols // 2, dtype=torch.uint8, device=DEV), torch.empty(rows, mx.pitch(cols), dtype=torch.uint8, device=DEV)
+    moe.moe_mx_quantize(rows, cols, 0, x, cols, mx.E2M1, q, s)
+    c, sc = mx.quantize(f64(x[-3:]), mx.E2M1)
+    assert (q[-3:].cpu().numpy() == mx.pack(c, mx.E2M1)).all() and (s[-3:].cpu().numpy() == mx.scale_rows(sc)).all()
+    T, d = rows * 2, cols // 2                                   # the same memory as rows of 16384
+    h = x.view(T, d)
+    w = torch.ones(d, dtype=torch.bfloat16, device=DEV)
+    y = torch.empty_like(h)
+    moe.moe_rmsnorm(T, d, 0, h, d, 0, None, d, w, 1e-6, None, y, None, None)
+    v = f64(h[-2:])
+    n = v / np.sqrt((v * v).mean(axis=1, keepdims=True) + np.float64(np.float32(1e-6)))
+    assert (np.abs(f64(y[-2:]) - n) <= (2.0 ** -8 + 4 * 2.0 ** -24) * np.abs(n)).all()
+    del x, h, y, q, s
+    rng = np.random.default_rng(8)
+    S, K, N = 33000, 128, 65536
+    W = mx.Matrix(rng, (1, N, K), mx.E2M1)
+    few = mx.Matrix(rng, (8, K), mx.E4M3)
+    xq, xs = few.q.repeat(S // 8, 1), few.s.repeat(S // 8, 1)
+    out, ws = torch.empty(S, N, dtype=torch.bfloat16, device=DEV), ws_for(S, 1, N)
+    moe.moe_mx_product(S, K, 1, N, mx.E4M3, xq, xs, None, W.q, W.s, 0, out, ws)
+    ok(ws)
+    ref, mag = product_ref(few.v, W.v, [8])
+    tol = K * 2.0 ** -23 * mag * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(ref)
+    assert (np.abs(f64(out[-8:]) - ref) <= tol).all()
+    assert torch.equal(out[:8], out[-8:])
+
+
 # ------------------------------------------------------------ used together
 
 def layer(rng, T, d, E, f, k):
@@ -377,8 +441,8 @@ def layer(rng, T, d, E, f, k):
     return p
 
 
-def forward(p, T, d, E, f, k, out, ws, h_out=None, delta=True, stream=None):
-    moe.moe_forward_mx(T, d, E, f, k, p["h"], p["delta"] if delta else None, p["w"], 1e-6, h_out, p["Wg"], None, p["W1"].q,
+def forward(p, T, d, E, f, k, out, ws, h_out=None, delta=True, stream=None, bias=None):
+    moe.moe_forward_mx(T, d, E, f, k, p["h"], p["delta"] if delta else None, p["w"], 1e-6, h_out, p["Wg"], bias, p["W1"].q,
                        p["W1"].s, p["W3"].q, p["W3"].s, p["W2"].q, p["W2"].s, out, ws, stream=stream)
 
 
@@ -443,6 +507,39 @@ def test_forward_is_the_composition_and_the_formula(T, d, E, f, k, delta):
             tol[t] += wt * (2.0 ** -8 * np.abs(y) + 2.0 ** -3 * np.sqrt((p["W2"].v[e] ** 2 @ hv ** 2) * 1e-3)
                             + (d + f) * 2.0 ** -23 * (np.abs(p["W2"].v[e]) @ np.abs(hv)))
     assert (np.abs(f64(out) - ref) <= tol * 4 + 1e-12).all()
+
+
+def test_forward_with_a_bias_and_in_place():
+    """A router bias that sends every token to experts 1 and 6, and the
+    residual stream updated where it stands."""
+    T, d, E, f, k = 70, 256, 8, 256, 2
+    p = layer(np.random.default_rng(2), T, d, E, f, k)
+    bias = torch.full((E,), -1e4, device=DEV)
+    bias[[1, 6]] = 1e4
+    out, ws = torch.empty(T, d, device=DEV), byte(moe.moe_forward_mx_workspace_size(T, d, E, f, k))
+    want = (p["h"].float() + p["delta"]).to(torch.bfloat16)
+    stored = p["h"].clone()
+    forward(p, T, d, E, f, k, out, ws, bias=bias)
+    assert torch.equal(p["h"], stored)
+    first = out.clone()
+    forward(p, T, d, E, f, k, out, ws, p["h"], bias=bias)
+    ok(ws)
+    assert torch.equal(p["h"], want) and torch.equal(out, first)
+    # the norm's bf16 rows through the two experts, in 64 bits from its 8-bit rows
+    ho, y, q, s = torch.empty_like(want), torch.empty_like(want), byte(T, d), byte(T, mx.pitch(d))
+    moe.moe_rmsnorm(T, d, 0, want, d, 0, None, d, p["w"], 1e-6, ho, y, q, s)
+    xv = mx.values(q.cpu().numpy().astype(np.int64), s[:, :d // 32].cpu().numpy().astype(np.int64), mx.E4M3)
+    a = f64(y) @ f64(p["Wg"]).T + f64(bias)
+    e = np.exp(a[:, [1, 6]] - a[:, [1, 6]].max(axis=1, keepdims=True))
+    wt = e / e.sum(axis=1, keepdims=True)
+    ref = np.zeros((T, d))
+    for i, j in enumerate((1, 6)):
+        g, b = xv @ p["W1"].v[j].T, xv @ p["W3"].v[j].T
+        c, sc = mx.quantize(g / (1 + np.exp(-g)) * b, mx.E4M3)
+        ref += wt[:, i:i + 1] * (mx.values(c, sc, mx.E4M3) @ p["W2"].v[j].T)
+    # logits near 1e4 are known to 2^-24 * 1e4 * a few (the weights to that),
+    # rows are rounded to bf16, few codes of h differ by a step
+    assert np.abs(f64(out) - ref).max() <= 2.0 ** -6 * np.abs(ref).max()
 
 
 def test_forward_in_graphs_and_on_streams():
