@@ -11,10 +11,11 @@
 //
 // Both read every input once and write every output once, and are bound by
 // that: the norm of 16384 x 4096 bf16 rows with an fp32 delta and every output
-// takes 109 us (6.8 TB/s), the quantisation of 114688 x 4096 bf16 values to
-// e2m1 with their values written back 315 us (6.7 TB/s), 4097 x 4096 to e4m3
-// 10 us (in L2), one row of 4096 2.4 us, the latency of a launch and of two
-// rounds through memory.
+// takes 108 us (6.8 TB/s; 113 us in long runs), the quantisation of 114688 x
+// 4096 bf16 values to e2m1 with their values written back 314 us (6.8 TB/s;
+// 350 us in long runs, at a clock that the power cap lowers), 4097 x 4096 to
+// e4m3 10 us (in L2), one row of 4096 2.4 us, the latency of a launch and of
+// two rounds through memory.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -52,9 +53,9 @@ __device__ __forceinline__ uint32_t block_code(const float (&v)[8])
 }
 
 // One CTA per row, V vectors of eight values per thread, held in registers
-// between the sum and the outputs, so a row is read once; V grows with d only
-// to stay within 512 threads, since more CTAs of shorter rows keep more loads
-// in flight.  The squares are summed in fp64: the conversions hide behind the
+// between the sum and the outputs, so a row is read once.  Long runs are held
+// by the power cap, and two vectors a thread do the same loads with less
+// (16384 x 4096: one vector 123 us, two 113, four 115).  The squares are summed in fp64: the conversions hide behind the
 // loads, and the statistic is right for every input, also one whose squares
 // leave fp32's range.
 template <int TYPE, int DELTA, int V>
@@ -145,6 +146,7 @@ __global__ void rmsnorm_kernel(const NormParams p)
 
 struct QuantParams {
     uint32_t total, nvec;  // vectors of eight in all, and per row
+    uint32_t step_row, step_col;  // kQuantThreads vectors on, in rows and columns
     int pitch;
     const uint8_t *x;
     long long x_stride;    // bytes
@@ -162,13 +164,24 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantPara
     constexpr int kCode = FMT == kMxE4M3 ? 8 : 4;
     const uint32_t base = blockIdx.x * (kQuantThreads * kQuantVec) + threadIdx.x;
     Vec8<TYPE> xv[kQuantVec];
+    // One division a thread: 351 us instead of 357 for 114688 x 4096 in long
+    // runs, which the power cap holds.
     uint32_t row[kQuantVec], col[kQuantVec];
+    row[0] = base / p.nvec;
+    col[0] = base - row[0] * p.nvec;
+#pragma unroll
+    for (int u = 1; u < kQuantVec; ++u) {
+        row[u] = row[u - 1] + p.step_row;
+        col[u] = col[u - 1] + p.step_col;
+        if (col[u] >= p.nvec) {
+            col[u] -= p.nvec;
+            ++row[u];
+        }
+    }
     ptx::grid_dep_wait();
 #pragma unroll
     for (int u = 0; u < kQuantVec; ++u) {
         const uint32_t i = base + u * kQuantThreads;
-        row[u] = i / p.nvec;
-        col[u] = i - row[u] * p.nvec;
         if (i < p.total)
             xv[u] = load8<TYPE>(p.x + row[u] * p.x_stride + static_cast<size_t>(col[u]) * kBytes);
     }
@@ -199,7 +212,7 @@ __global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantPara
 template <int TYPE, int DELTA>
 cudaError_t norm_v(const NormParams &p, int T, cudaStream_t s, bool pdl)
 {
-    const int v = p.nvec <= 512 ? 1 : p.nvec <= 1024 ? 2 : 4;
+    const int v = p.nvec <= 256 ? 1 : p.nvec <= 1024 ? 2 : 4;
     const int thr = ((p.nvec + v - 1) / v + 31) / 32 * 32;
     auto *k = v == 1 ? rmsnorm_kernel<TYPE, DELTA, 1>
               : v == 2 ? rmsnorm_kernel<TYPE, DELTA, 2> : rmsnorm_kernel<TYPE, DELTA, 4>;
@@ -258,6 +271,8 @@ cudaError_t launch_mx_quantize(const MxQuantLaunch &a, cudaStream_t s)
     QuantParams p{};
     p.nvec = static_cast<uint32_t>(a.cols / 8);
     p.total = static_cast<uint32_t>(a.rows) * p.nvec;
+    p.step_row = kQuantThreads / p.nvec;
+    p.step_col = kQuantThreads % p.nvec;
     p.pitch = mx_scale_pitch(a.cols);
     p.x = static_cast<const uint8_t *>(a.x);
     p.x_stride = a.x_stride * size_of(a.type);

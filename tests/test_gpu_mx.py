@@ -121,6 +121,18 @@ def test_rmsnorm_matches_formula(type, dt, T, d, extra):
     assert torch.equal(y, y2) and torch.equal(q, q2) and torch.equal(s, s2)
 
 
+@pytest.mark.parametrize("type,size", [(0, 3e30), (0, 1e-25), (0, 3e38), (1, 6e4), (1, 1e-7)])
+def test_rmsnorm_of_16_bit_extremes(type, size):
+    """Squares that leave fp32's range, above and below."""
+    t, T, d = mx.TORCH[type], 3, 1376
+    h = (torch.randn(T, d, generator=torch.Generator(device=DEV).manual_seed(5), device=DEV).clamp(-1, 1) * size).to(t)
+    w, y, eps = torch.ones(d, dtype=t, device=DEV), torch.empty(T, d, dtype=t, device=DEV), 1e-38
+    moe.moe_rmsnorm(T, d, type, h, d, type, None, d, w, eps, None, y, None, None)
+    v = f64(h)
+    n = v / np.sqrt((v * v).mean(axis=1, keepdims=True) + np.float64(np.float32(eps)))
+    assert (np.abs(f64(y) - n) <= (HALF[t] + 4 * 2.0 ** -24) * np.abs(n) + TINY[t]).all()
+
+
 def test_rmsnorm_in_place_and_extremes():
     d = 256
     h = torch.zeros(6, d, device=DEV)
