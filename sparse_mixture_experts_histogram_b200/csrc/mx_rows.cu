@@ -11,7 +11,7 @@
 //
 // Both read every input once and write every output once, and are bound by
 // that: the norm of 16384 x 4096 bf16 rows with an fp32 delta and every output
-// takes 108 us (6.8 TB/s; 113 us in long runs), the quantisation of 114688 x
+// takes 110 us (6.7 TB/s; 113 us in long runs), the quantisation of 114688 x
 // 4096 bf16 values to e2m1 with their values written back 314 us (6.8 TB/s;
 // 350 us in long runs, at a clock that the power cap lowers), 4097 x 4096 to
 // e4m3 10 us (in L2), one row of 4096 2.4 us, the latency of a launch and of
