@@ -82,7 +82,7 @@ constexpr size_t kCounters = static_cast<size_t>(kMaxPairs) * 2 * kEpiWarps;
 // of the MMA warp: kAtoms 128-byte columns of both operands, whose MMAs it
 // issues in one straight run behind one wait.  (Waits and branches between
 // fewer MMAs cost more than the MMAs of a narrow tile: 2000 rows over 256
-// experts of 2048 -> 7168, e4m3, 4 MMAs a run 414 us, 8 a run 344 us.)
+// experts of 2048 -> 7168, e4m3, 4 MMAs a run 414 us, 8 a run 355 us.)
 template <int FMT, int NMAX>
 struct Shape {
     static constexpr int kAtoms = 2;
@@ -450,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // the warps that issue copies and MMAs then keep addresses, descriptors
     // and loop counters in uniform registers, which those instructions read.
     // With one thread's own values every operand was moved over before each
-    // MMA: 150 cycles an MMA instead of 90.
+    // MMA: 150 cycles an MMA instead of 97.
     const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0);
     const int lane = threadIdx.x & 31;
     const uint32_t cta = __shfl_sync(0xffffffffu, ptx::cluster_ctarank(), 0);  // 0: issues the MMAs
@@ -461,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint64_t *full = reinterpret_cast<uint64_t *>(reinterpret_cast<uint8_t *>(xchg) + kXchg);
     uint64_t *empty = full + kStages;
     uint64_t *cfull = empty + kStages;      // [kScSlots] scale chunk in shared memory
-    uint64_t *cempty = cfull + SM::kScSlots;    // [SM::kScSlots]
+    uint64_t *cempty = cfull + SM::kScSlots;  // [kScSlots]
     uint64_t *tfull = cempty + SM::kScSlots;  // [kAccs] accumulator
     uint64_t *tempty = tfull + SM::kAccs;   // [kAccs]
     uint64_t *sfull = tempty + SM::kAccs;   // [kScBufs] scales in tensor memory

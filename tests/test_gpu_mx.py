@@ -175,6 +175,7 @@ SIZES = [
     ([1], 128, 8), ([3], 256, 136), ([2, 0, 1], 128, 1000), ([0, 5, 0, 0], 384, 264),
     ([37, 0, 128, 1, 200, 64], 640, 392), ([191, 193, 192], 512, 520), ([700, 16], 1408, 264),
     ([1] * 40, 256, 256), ([2, 1], 14336, 512), ([17] * 9, 2048, 640),
+    ([80], 384, 264), ([70, 60], 640, 136), ([95], 128, 16),
     ([5, 4], 640, 72), ([4, 3], 384, 24), ([20], 1152, 40), ([3] * 5, 896, 264), ([7, 9, 1], 1536, 520),
     ([1], 4096, 256), ([0, 3], 3584, 8), ([1] * 75, 3200, 256),   # cut units of fewer chunks than there are CTA pairs
 ]
@@ -622,3 +623,16 @@ def test_every_operator_in_one_graph_after_a_memset():
         assert (np.abs(f64(y) - n) <= 5 * 2.0 ** -24 * np.abs(n)).all()
         c, sc = mx.quantize(f64(y), mx.E2M1)
         assert (q4.cpu().numpy() == mx.pack(c, mx.E2M1)).all() and (s4.cpu().numpy() == mx.scale_rows(sc)).all()
+
+
+def test_the_examples_of_the_readme_run():
+    import os
+    import re
+    text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")).read()
+    blocks = [b for b in re.findall(r"```python\n(.*?)```", text, re.S) if "moe." in b]
+    assert len(blocks) == 2
+    names = {}
+    exec("\n".join(blocks), names)
+    torch.cuda.synchronize()
+    assert names["out"].isfinite().all() and names["stream"].isfinite().all()
+    assert moe.moe_get_device_error(names["ws"])[0] == 0
