@@ -230,10 +230,12 @@ struct Walk {
 
     __device__ __forceinline__ int owner(int item) const { return ((item + 1) * cutters - 1) / items; }
 
-    // Next unit and its chunks; false when the pair is done.
+    // Next unit and its chunks; false when the pair is done.  Cut units come
+    // first, so that whole ones hide the joining of their parts.
     __device__ __forceinline__ bool next(Work &w, int &unit)
     {
-        if (u < whole) {
+        if (it >= end) {
+            if (u >= whole) return false;
             unit = u;
             u += pairs;
             w.c0 = 0;
@@ -241,7 +243,6 @@ struct Walk {
             w.part = -1;
             return true;
         }
-        if (it >= end) return false;
         const int c = it / chunks;
         const int base = c * chunks;
         unit = whole + c;
