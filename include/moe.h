@@ -50,7 +50,8 @@
  *   and moe_expert_ffn_static assign work to CTAs statically; a CTA that
  *   waits on another CTA's results spins (bounded) on the assumption that
  *   all CTAs of the launch are resident, which holds when the layer has the
- *   GPU to itself.  If other work keeps SMs occupied for longer than the
+ *   GPU to itself (the microscaled products wait for no CTA outside a pair's
+ *   cluster).  If other work keeps SMs occupied for longer than the
  *   bound (2 s), the wait gives up with MOE_DEVERR_TIMEOUT_EPI.
  * Errors: arguments are checked on the host before anything is launched;
  *   the first failed check is returned and nothing is enqueued.  A failed
