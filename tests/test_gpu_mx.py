@@ -636,3 +636,225 @@ def test_the_examples_of_the_readme_run():
     torch.cuda.synchronize()
     assert names["out"].isfinite().all() and names["stream"].isfinite().all()
     assert moe.moe_get_device_error(names["ws"])[0] == 0
+
+
+# ------------------------------------------- sums that meet in the workspace
+# Units that do not fill the last turn of the CTA pairs are cut along K where
+# that saves more than it costs, by the number of units, the chunks of 512 in
+# K and the rows of the call.  A workspace holds, behind the header of 256
+# bytes, one counter for every cut unit, CTA and epilogue warp (80 x 2 x 8),
+# which says how many of the unit's parts have come in.
+
+COUNTERS = 80 * 2 * 8 * 4
+
+
+def cut_units(ws, at=256):
+    """How many units the last call on the workspace cut (a call that can cut
+    none leaves the counters alone)."""
+    c = ws[at:at + COUNTERS].view(torch.int32).view(80, 16)
+    return int((c > 0).any(dim=1).sum())
+
+
+def units(sizes, N, rows_blk, S):
+    """Units of a launch: tiles of at most 96 or 192 rows times blocks of N."""
+    most = 96 if -(-S // len(sizes)) <= 64 else 192
+    return sum(-(-n // most) for n in sizes) * -(-N // rows_blk)
+
+
+class Codes:
+    """Random 4-bit weights [E, rows, cols] of about the size cols^-1/2, made
+    on the GPU: `q`, `s` as the library takes them, `v` their fp64 values."""
+
+    def __init__(self, g, E, rows, cols):
+        self.q = torch.randint(0, 256, (E, rows, cols // 2), generator=g, device=DEV, dtype=torch.uint8)
+        self.s = torch.zeros(E, rows, mx.pitch(cols), dtype=torch.uint8, device=DEV)
+        self.s[..., :cols // 32] = 127 - round(np.log2(3 * cols ** 0.5)) + \
+            torch.randint(0, 2, (E, rows, cols // 32), generator=g, device=DEV, dtype=torch.uint8)
+        self.cols = cols
+
+    def matrix(self, e):
+        v = torch.from_numpy(np.concatenate([mx.grid(mx.E2M1), -mx.grid(mx.E2M1)])).to(DEV)
+        c = torch.stack([self.q[e] & 15, self.q[e] >> 4], dim=-1).flatten(-2).long()
+        s = torch.exp2(self.s[e, :, :self.cols // 32].double() - 127)
+        return v[c] * s.repeat_interleave(32, dim=-1)
+
+
+def codes_ref(x, W, sizes):
+    """(y, sum of magnitudes) in 64 bits, on the GPU, of fp64 rows and Codes."""
+    y, a, r = [], [], 0
+    for e, n in enumerate(sizes):
+        if n:
+            m, rows = W.matrix(e), torch.from_numpy(x[r:r + n]).to(DEV)
+            y.append(rows @ m.T), a.append(rows.abs() @ m.abs().T)
+        r += n
+    return torch.cat(y).cpu().numpy(), torch.cat(a).cpu().numpy()
+
+
+CUT = [
+    ([40], 8192, 512), ([33, 0, 40], 10240, 264), ([100, 5], 16384, 136),   # tiles of at most 96 rows
+    ([80], 8192, 264), ([190], 16384, 24), ([200, 100], 16384, 264),        # of at most 192 rows
+    ([1] * 5, 4096, 4096), ([9, 0, 30, 17, 3, 1], 8192, 4096),   # six of 80 units cut, the others whole
+]
+
+
+@pytest.mark.parametrize("fmt", [mx.E4M3, mx.E2M1])
+@pytest.mark.parametrize("sizes,K,N", CUT)
+@pytest.mark.parametrize("yt", [0, 2])
+@pytest.mark.parametrize("behind", [0, 2])
+def test_product_of_cut_units_matches_formula(fmt, sizes, K, N, yt, behind):
+    rng = np.random.default_rng(len(sizes) + K + N)
+    E, R = len(sizes), sum(sizes)
+    S = R + behind                                 # rows behind the last segment
+    x = mx.Matrix(rng, (S, K), fmt)
+    x.s[R:] = 0xFF
+    W = Codes(torch.Generator(device=DEV).manual_seed(K + N), E, N, K)
+    t = mx.TORCH[yt]
+    y = torch.full((S, N), 7.0, dtype=t, device=DEV)
+    ws = ws_for(S, E, N)
+    args = (S, K, E, N, fmt, x.q, x.s, segments(sizes), W.q, W.s, yt)
+    moe.moe_mx_product(*args, y, ws)
+    ok(ws)
+    n = cut_units(ws)
+    assert 0 < n <= units(sizes, N, 256, S)
+    if units(sizes, N, 256, S) >= 80:
+        assert n < units(sizes, N, 256, S)
+    assert (y[R:] == 7).all()
+    ref, mag = codes_ref(x.v[:R], W, sizes)
+    err = np.abs(f64(y[:R]) - ref)
+    assert (err <= K * 2.0 ** -23 * mag * (1 + HALF[t]) + HALF[t] * np.abs(ref)).all()
+    for _ in range(3):                             # the same workspace again: the same bits
+        y2 = torch.full((S, N), 7.0, dtype=t, device=DEV)
+        moe.moe_mx_product(*args, y2, ws)
+        assert torch.equal(y, y2)
+    ok(ws)
+
+
+@pytest.mark.parametrize("fmt", [mx.E4M3, mx.E2M1])
+@pytest.mark.parametrize("sizes,K,N", [([40], 8192, 512), ([150], 16384, 264), ([9, 0, 30, 17, 3, 1], 8192, 4096)])
+def test_cut_units_lose_no_product(fmt, sizes, K, N):
+    """Whole numbers: every sum is one below 2^24, so the result is exact
+    whatever the order, and a chunk left out or counted twice shows."""
+    rng = np.random.default_rng(K + N)
+    E, S = len(sizes), sum(sizes)
+    one = 0x38 if fmt == mx.E4M3 else 2                           # the code of 1
+    xq = one * rng.integers(0, 2, (S, K))
+    x = torch.from_numpy((xq > 0).astype(np.float64)).to(DEV)
+    W = Codes(torch.Generator(device=DEV).manual_seed(K + N), E, N, K)
+    W.q &= 0xAA                                                   # 0, 1, -0, -1
+    W.s[..., :K // 32] = 127
+    xs = torch.from_numpy(mx.scale_rows(np.full((S, K // 32), 127))).to(DEV)
+    y, ws = torch.empty(S, N, device=DEV), ws_for(S, E, N)
+    moe.moe_mx_product(S, K, E, N, fmt, torch.from_numpy(mx.pack(xq, fmt)).to(DEV), xs, segments(sizes), W.q, W.s, 2, y, ws)
+    ok(ws)
+    assert cut_units(ws) > 0
+    r = 0
+    for e, n in enumerate(sizes):
+        assert torch.equal(y[r:r + n].double(), x[r:r + n] @ W.matrix(e).T), e
+        r += n
+
+
+@pytest.mark.parametrize("fmt", [mx.E4M3, mx.E2M1])
+@pytest.mark.parametrize("act", [0, 1])
+@pytest.mark.parametrize("sizes,d,f", [([40], 8192, 128), ([100], 16384, 256), ([190], 16384, 128), ([150, 60], 16384, 128),
+                                       ([1] * 5, 4096, 2048), ([9, 0, 30, 17, 3, 1], 8192, 2048)])
+def test_gated_of_cut_units_matches_formula(fmt, act, sizes, d, f):
+    rng = np.random.default_rng(len(sizes) + d + f)
+    E, R = len(sizes), sum(sizes)
+    S = R + 2
+    x = mx.Matrix(rng, (S, d), fmt)
+    x.s[R:] = 0xFF
+    g = torch.Generator(device=DEV).manual_seed(d + f)
+    W1, W3 = Codes(g, E, f, d), Codes(g, E, f, d)
+    h = torch.full((S, f), 7.0, dtype=torch.bfloat16, device=DEV)
+    hq, hs = byte(S, f), byte(S, mx.pitch(f))
+    ws = ws_for(S, E, f)
+    args = (S, d, E, f, fmt, x.q, x.s, segments(sizes), W1.q, W1.s, W3.q, W3.s, act)
+    n = units(sizes, f, 128, S)
+    moe.moe_mx_gated(*args, h, None, None, ws)
+    ok(ws)
+    assert 0 < cut_units(ws) <= n and (n < 80 or cut_units(ws) < n)
+    moe.moe_mx_gated(*args, None, hq, hs, ws)
+    ok(ws)
+    assert 0 < cut_units(ws)
+    assert (h[R:] == 7).all() and (hq[R:] == 0xA5).all() and (hs[R:] == 0xA5).all()
+    # as in test_gated_matches_formula
+    (a, ma), (b, mb) = codes_ref(x.v[:R], W1, sizes), codes_ref(x.v[:R], W3, sizes)
+    g = 1 / (1 + np.exp(-a)) * (1 if act else a)
+    ref = g * b
+    da, db = d * 2.0 ** -23 * ma, d * 2.0 ** -23 * mb
+    tol = 1.1 * da * np.abs(b) + np.abs(g) * db + 1.1 * da * db + 2.0 ** -17 * np.abs(ref)
+    assert (np.abs(f64(h[:R]) - ref) <= tol + 2.0 ** -8 * (np.abs(ref) + tol)).all()
+    sc = hs[:R, :f // 32].cpu().numpy().astype(np.int64)
+    blocks, tb = np.abs(ref).reshape(R, -1, 32), tol.reshape(R, -1, 32)
+    lo = mx.scale_code(np.maximum(blocks - tb, 0).max(axis=2), mx.E4M3)
+    hi = mx.scale_code((blocks + tb).max(axis=2), mx.E4M3)
+    assert ((sc >= lo) & (sc <= hi)).all()
+    v = mx.values(hq[:R].cpu().numpy().astype(np.int64), sc, mx.E4M3)
+    half = np.maximum(2.0 ** -4 * (np.abs(ref) + tol), 2.0 ** -10 * np.repeat(mx.scale_value(sc), 32, axis=1))
+    assert (np.abs(v - ref) <= tol + half).all()
+    for _ in range(3):
+        h2, q2, s2 = torch.full_like(h, 7.0), byte(S, f), byte(S, mx.pitch(f))
+        moe.moe_mx_gated(*args, h2, None, None, ws)
+        moe.moe_mx_gated(*args, None, q2, s2, ws)
+        assert torch.equal(h, h2) and torch.equal(hq, q2) and torch.equal(hs, s2)
+    ok(ws)
+
+
+# rows, widths and experts of which both products cut units: all of them (6144
+# -> 4096, one expert hit), and two of 150 in the up projections (4096 -> 9600)
+@pytest.mark.parametrize("T,d,E,f,k", [(1, 6144, 2, 4096, 1), (1, 4096, 2, 9600, 2), (3, 4096, 2, 9600, 2)])
+def test_forward_of_cut_units(T, d, E, f, k):
+    """The layer's own counters and scratch: a workspace filled with ones, the
+    same one again on other inputs, and replayed from a graph."""
+    g = torch.Generator(device=DEV).manual_seed(T + d)
+    S = T * k
+    p = dict(h=None, delta=None, w=(1 + 0.1 * torch.randn(d, generator=g, device=DEV)).to(torch.bfloat16),
+             Wg=(torch.randn(E, d, generator=g, device=DEV) * d ** -0.5).to(torch.bfloat16),
+             W1=Codes(g, E, f, d), W3=Codes(g, E, f, d), W2=Codes(g, E, d, f))
+    inputs = [(torch.randn(T, d, generator=g, device=DEV).to(torch.bfloat16), torch.randn(T, d, generator=g, device=DEV))
+              for _ in range(3)]
+    ws = byte(moe.moe_forward_mx_workspace_size(T, d, E, f, k), fill=0xFF)
+    outs = []
+    for h, delta in inputs + inputs[:1]:
+        p.update(h=h, delta=delta)
+        out = torch.full((T, d), float("nan"), device=DEV)
+        forward(p, T, d, E, f, k, out, ws)
+        ok(ws)
+        # behind the header and the router's tile counter
+        assert cut_units(ws, 512) > 0 and cut_units(ws, 512 + COUNTERS) > 0
+        outs.append(out)
+    assert torch.equal(outs[0], outs[3])
+    src_h, src_delta = torch.empty_like(inputs[0][0]), torch.empty_like(inputs[0][1])
+    p.update(h=src_h, delta=src_delta)
+    out = torch.empty(T, d, device=DEV)
+    src_h.copy_(inputs[0][0]), src_delta.copy_(inputs[0][1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        forward(p, T, d, E, f, k, out, ws)
+    for (h, delta), want in list(zip(inputs, outs)) * 2:
+        src_h.copy_(h), src_delta.copy_(delta)
+        out.fill_(float("nan"))
+        graph.replay()
+        assert torch.equal(out, want)
+    ok(ws)
+    # the separate calls, and the formula in 64 bits from their rows and routing
+    for (h, delta), out in zip(inputs[:2], outs):
+        p.update(h=h, delta=delta)
+        want, _, q, s, idx, w = composed(p, T, d, E, f, k)
+        assert torch.allclose(out, want, rtol=0, atol=float(want.abs().max()) * k * 2.0 ** -23)
+        xv = torch.from_numpy(mx.values(q.cpu().numpy().astype(np.int64), s[:, :d // 32].cpu().numpy().astype(np.int64), mx.E4M3)).to(DEV)
+        ref, tol = torch.zeros(T, d, dtype=torch.float64, device=DEV), torch.zeros(T, d, dtype=torch.float64, device=DEV)
+        for t in range(T):
+            for j in range(k):
+                e, wt = int(idx[t, j]), float(w[t, j])
+                a, b = p["W1"].matrix(e) @ xv[t], p["W3"].matrix(e) @ xv[t]
+                hh = a * torch.sigmoid(a) * b
+                c, sc = mx.quantize(f64(hh)[None], mx.E4M3)
+                hv = torch.from_numpy(mx.values(c, sc, mx.E4M3)[0]).to(DEV)
+                W2 = p["W2"].matrix(e)
+                y = W2 @ hv
+                ref[t] += wt * y
+                # as in test_forward_is_the_composition_and_the_formula
+                tol[t] += wt * (2.0 ** -8 * y.abs() + 2.0 ** -3 * torch.sqrt((W2 ** 2 @ hv ** 2) * 1e-3)
+                                + (d + f) * 2.0 ** -23 * (W2.abs() @ hv.abs()))
+        assert ((out.double() - ref).abs() <= tol * 4 + 1e-12).all()
