@@ -36,6 +36,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "gate.cuh"
 #include "internal.h"
 #include "launch.cuh"
 
@@ -545,16 +546,28 @@ __global__ void __launch_bounds__(kThreads, 1)
                     ptx::tmem_ld8(tb + static_cast<uint32_t>(BN + c0), b);
                     ptx::tc_wait_ld();
                     uint8_t *hrow = hb + c0 * 128;
+                    float most = 0.0f;
 #pragma unroll
                     for (int jt = 0; jt < 8; ++jt) {
                         if (c0 + jt < it.valid) {
                             const float gv = __uint_as_float(a[jt]);
                             const float bv = __uint_as_float(b[jt]);
-                            const float h = __fdividef(p.act ? bv : gv * bv, 1.0f + __expf(-gv));
+                            const float h = gate_mul(gv, bv, p.act, most);
                             // row c0+jt (c0 is a multiple of 8, so the row's swizzle
                             // phase is jt), column f, 128-byte-swizzled layout
                             *reinterpret_cast<__nv_bfloat16 *>(hrow + jt * 128 + ((hchunk ^ jt) << 4)) =
                                 __float2bfloat16_rn(h);
+                        }
+                    }
+                    if (__any_sync(0xffffffffu, most >= kGateRange)) {
+#pragma unroll 1
+                        for (int jt = 0; jt < 8 && c0 + jt < it.valid; ++jt) {
+                            const uint32_t col = tb + static_cast<uint32_t>(c0 + jt);
+                            const uint32_t gv = ptx::tmem_ld1(col), bv = ptx::tmem_ld1(col + BN);
+                            ptx::tc_wait_ld();
+                            *reinterpret_cast<__nv_bfloat16 *>(hrow + jt * 128 + ((hchunk ^ jt) << 4)) =
+                                __float2bfloat16_rn(
+                                    gate_redo(__uint_as_float(gv), __uint_as_float(bv), p.act));
                         }
                     }
                 }

@@ -38,6 +38,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "gate.cuh"
 #include "internal.h"
 #include "launch.cuh"
 
@@ -469,14 +470,25 @@ __global__ void __launch_bounds__(kFfnThreads, 1)
                 ptx::tc_wait_ld();
                 if (w.up) {
                     const int f = w.blk * 128 + row_in_blk;
+                    float most = 0.0f;
 #pragma unroll
                     for (int j = 0; j < 32; ++j) {
                         if (c0 + j < w.valid) {
                             const float g = __uint_as_float(a[j]);
                             const float bv = __uint_as_float(b[j]);
-                            const float h = __fdividef(p.act ? bv : g * bv, 1.0f + __expf(-g));
+                            const float h = gate_mul(g, bv, p.act, most);
                             p.H[static_cast<size_t>(w.r0 + c0 + j) * p.d_ff + f] =
                                 __float2bfloat16_rn(h);
+                        }
+                    }
+                    if (__any_sync(0xffffffffu, most >= kGateRange)) {
+#pragma unroll 1
+                        for (int j = 0; j < 32 && c0 + j < w.valid; ++j) {
+                            const uint32_t col = tb + static_cast<uint32_t>(c0 + j);
+                            const uint32_t g = ptx::tmem_ld1(col), bv = ptx::tmem_ld1(col + BN);
+                            ptx::tc_wait_ld();
+                            p.H[static_cast<size_t>(w.r0 + c0 + j) * p.d_ff + f] = __float2bfloat16_rn(
+                                gate_redo(__uint_as_float(g), __uint_as_float(bv), p.act));
                         }
                     }
                 } else {

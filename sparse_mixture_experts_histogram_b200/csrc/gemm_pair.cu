@@ -53,6 +53,7 @@
 #include <atomic>
 
 #include "common.cuh"
+#include "gate.cuh"
 #include "internal.h"
 #include "launch.cuh"
 
@@ -214,12 +215,6 @@ __device__ __forceinline__ int warp_scan_incl(int v, int lane)
         if (lane >= off) v += n;
     }
     return v;
-}
-
-// silu(g) * b (act 0) or sigmoid(g) * b (act 1).
-__device__ __forceinline__ float gate_mul(float g, float b, int act)
-{
-    return __fdividef(act ? b : g * b, 1.0f + __expf(-g));
 }
 
 __global__ void __launch_bounds__(kPThreads, 1)
@@ -571,6 +566,7 @@ __global__ void __launch_bounds__(kPThreads, 1)
                     // adjacent columns of one row at a time.
                     const int t0 = c * kPChunk + (is_a ? 0 : 8);
                     __nv_bfloat16 *hrow = p.H + static_cast<size_t>(w.r0 + t0) * p.d_ff + hcol;
+                    float most = 0.0f;
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
                         const float o = theirs[j * 32 + lane];
@@ -578,7 +574,17 @@ __global__ void __launch_bounds__(kPThreads, 1)
                         const float b = is_a ? o : __uint_as_float(r[8 + j]);
                         if (t0 + j < w.valid)
                             hrow[static_cast<size_t>(j) * p.d_ff] =
-                                __float2bfloat16_rn(gate_mul(g, b, p.act));
+                                __float2bfloat16_rn(gate_mul(g, b, p.act, most));
+                    }
+                    if (__any_sync(0xffffffffu, most >= kGateRange)) {
+#pragma unroll 1
+                        for (int j = 0; j < 8 && t0 + j < w.valid; ++j) {
+                            const float own = __uint_as_float(ptx::tmem_ld1(tb + static_cast<uint32_t>(t0 + j)));
+                            ptx::tc_wait_ld();
+                            const float o = theirs[j * 32 + lane];
+                            hrow[static_cast<size_t>(j) * p.d_ff] = __float2bfloat16_rn(
+                                gate_redo(is_a ? own : o, is_a ? o : own, p.act));
+                        }
                     }
                 }
                 if (stop) break;

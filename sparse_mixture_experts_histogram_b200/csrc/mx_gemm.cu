@@ -54,6 +54,7 @@
 #include <atomic>
 
 #include "common.cuh"
+#include "gate.cuh"
 #include "internal.h"
 #include "launch.cuh"
 #include "mx.cuh"
@@ -328,12 +329,6 @@ __device__ __forceinline__ int warp_scan_incl(int v, int lane)
 }
 
 // ----------------------------------------------------------------- epilogue
-// silu(g) * b (act 0) or sigmoid(g) * b (act 1).
-__device__ __forceinline__ float gate_mul(float g, float b, int act)
-{
-    return __fdividef(act ? b : g * b, 1.0f + __expf(-g));
-}
-
 // NC accumulator columns of 32 lanes to rows t0 .. t0+NC-1 of y in bf16: lane
 // pairs swap so that each lane stores two neighbouring output columns.
 template <int NC>
@@ -907,7 +902,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // a warps keep tokens 0..7 of the chunk and hand 8..15
                         // to their b partner; b warps the other way round.
                         float *mine = xa + xb * (2 * 8 * 32) + (is_a ? 0 : 8 * 32) + lane;
-                        const float *theirs = xa + xb * (2 * 8 * 32) + (is_a ? 8 * 32 : 0) + lane;
+                        float *theirs = xa + xb * (2 * 8 * 32) + (is_a ? 8 * 32 : 0) + lane;
                         if (is_a) {
 #pragma unroll
                             for (int j = 0; j < 8; ++j) mine[j * 32] = __uint_as_float(r[8 + j]);
@@ -923,17 +918,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                             stop = true;
                             break;
                         }
-                        float v[8];
+                        const int t0 = c * kColChunk + (is_a ? 0 : 8);
+                        float v[8], most = 0.0f;
                         if (is_a) {
 #pragma unroll
                             for (int j = 0; j < 8; ++j)
-                                v[j] = gate_mul(__uint_as_float(r[j]), theirs[j * 32], p.act);
+                                v[j] = gate_mul(__uint_as_float(r[j]), theirs[j * 32], p.act, most);
                         } else {
 #pragma unroll
                             for (int j = 0; j < 8; ++j)
-                                v[j] = gate_mul(theirs[j * 32], __uint_as_float(r[8 + j]), p.act);
+                                v[j] = gate_mul(theirs[j * 32], __uint_as_float(r[8 + j]), p.act, most);
                         }
-                        store_h8(p, v, w.r0, c * kColChunk + (is_a ? 0 : 8), w.lo, w.hi, o, lane);
+                        if (__any_sync(0xffffffffu, most >= kGateRange)) {
+                            // results take the place of the partner's values,
+                            // which only this lane reads
+#pragma unroll 1
+                            for (int j = 0; j < 8; ++j) {
+                                const float own = __uint_as_float(ptx::tmem_ld1(tb + static_cast<uint32_t>(t0 + j)));
+                                ptx::tc_wait_ld();
+                                const float got = theirs[j * 32];
+                                theirs[j * 32] = gate_redo(is_a ? own : got, is_a ? got : own, p.act);
+                            }
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) v[j] = theirs[j * 32];
+                        }
+                        store_h8(p, v, w.r0, t0, w.lo, w.hi, o, lane);
                         xb ^= 1;
                     } else {
                         float v[16];
@@ -998,7 +1007,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             }
                             if constexpr (GATED) {
 #pragma unroll
-                                for (int j = 0; j < 8; ++j) v[j] = gate_mul(v[j], u[j], p.act);
+                                for (int j = 0; j < 8; ++j) v[j] = gate_redo(v[j], u[j], p.act);
                                 store_h8(p, v, w.r0, c * kColChunk + h8, w.lo, w.hi, o, lane);
                             } else if (p.y_type == kTypeBf16) {
                                 store_bf16<8>(p, v, w.r0, c * kColChunk + h8, w.lo, w.hi, o, lane);
