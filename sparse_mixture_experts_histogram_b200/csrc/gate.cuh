@@ -10,6 +10,12 @@
 // value instead: 4096 tokens of d = 512, d_ff = 1024 82 us, this way 80 us.
 // gate_redo()'s second form for every value: 8192 microscaled rows of 4096 ->
 // 2 x 14336 773 us, this way 747 us.)
+//
+// Exponential and division are CUDA's fast ones, which are off by a few 2^-23
+// (the exponential by |g| 2^-24 more).  7.4e7 e4m3 values of 4096 -> 2 x 4096, of
+// which those count that are not the ones of 64 bits: 87 on e4m3 rows and 52 on
+// e2m1 rows; with rounded functions on the same sums 80 and 57, and the gated
+// prefill product 12 % slower.
 #pragma once
 
 namespace moe {

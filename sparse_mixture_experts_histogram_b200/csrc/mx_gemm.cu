@@ -38,13 +38,16 @@
 // scales.  All waits are bounded.
 //
 // What bounds it, at the rates of a plain copy (6.54 TB/s) and a bf16 library
-// product (1607 TFLOP/s) on the same card: few rows an expert, the weights'
-// bytes and, with e4m3 rows, the issue of MMAs (2000 rows over 256 experts of
-// 2048 -> 7168: 355 us, 5.7 TB/s; e2m1 rows 297 us, 6.8 TB/s); one token, the
-// latency of a launch's ends (14336 -> 4096, 2 experts: 22 us, of which 10 us are the
-// bytes); prefill, the operands' way from L2 through shared memory and the
-// power cap (8192 rows, 14336 -> 4096: 367 us, 2.6 PFLOP/s; e2m1 rows 198 us,
-// 4.9 PFLOP/s; gated 4096 -> 2 x 14336 with e4m3 out: 733 us, 2.6 PFLOP/s).
+// product (1607 TFLOP/s) on the same card.  Times are of 12 calls in a graph;
+// behind the slash those of runs of 0.15 s, in which the power cap lowers the
+// clock.  Few rows an expert, the weights' bytes and, with e4m3 rows, the issue
+// of MMAs (2000 rows over 256 experts of 2048 -> 7168: 353 us, 5.7 TB/s / 407 us,
+// 4.9 TB/s; e2m1 rows 297 us, 6.8 TB/s); one token, the latency of a launch's
+// ends (14336 -> 4096, 2 experts: 22 us, of which 10 us are the bytes); prefill,
+// the operands' way from L2 through shared memory and the power cap (8192 rows,
+// 14336 -> 4096: 377 us, 2.6 PFLOP/s / 443 us, 2.2 PFLOP/s; e2m1 rows 198 us,
+// 4.9 PFLOP/s; gated 4096 -> 2 x 14336 with e4m3 out: 754 us, 2.6 PFLOP/s /
+// 893 us, 2.2 PFLOP/s).
 //
 // Method: as gemm_pair.cu; the pages' deployment section (jsqmd.com) asks for
 // quantised experts.
@@ -274,7 +277,11 @@ struct Walk {
 // for 64, 30 us for 176, where a chunk takes about 1 us; it is taken where it
 // saves more chunks than that.  Measured: two rows of 14336 -> 4096 (28 chunks
 // down to 13) 33.5 us whole, 23.9 us cut; 64 rows of 2048 -> 4096 (4 down to
-// 1) 11 us whole, 19 us cut.
+// 1) 11 us whole, 19 us cut.  The columns charged for are those of the widest
+// tile that S rows allow, which the host knows too (it leaves the counters
+// uncleared where nothing can be cut), not of the widest that the segments
+// have: 64 rows spread one or two to an expert are charged for 64 columns, and
+// stay whole up to K = 5632.
 __host__ __device__ constexpr int join_chunks(int n) { return 2 + n / 8; }
 
 __device__ __forceinline__ int plan(int units, int pairs, int chunks, int n)
@@ -1133,6 +1140,9 @@ int tile_rows(const MxGemmLaunch &a)
     // Rows per expert if they were even.  16 experts of 4096 -> 4096 with
     // uneven segments, e4m3 rows, tiles of at most 96 / 192 rows: 8 rows an
     // expert 40 / 47 us, 32: 41 / 45, 64: 42 / 44, 80: 50 / 45, 96: 55 / 45.
+    // The number of units does not enter: a few wide segments of narrow
+    // weights (777 rows over 4 experts of 1408 -> 1000: 24 units) leave pairs
+    // idle.
     const int rows = (a.S + a.E - 1) / a.E;
     return rows <= 64 ? 96 : kMaxN;
 }
